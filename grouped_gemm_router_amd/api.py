@@ -27,7 +27,12 @@ EXPORTS = ["moe_status_string", "moe_abi_version", "moe_route_workspace_size", "
            "moe_permute", "moe_permute_noalloc", "moe_grouped_gemm_workspace_size",
            "moe_grouped_gemm",
            "moe_grouped_gemm_fp8", "moe_combine",
-           "moe_quantize_fp8"]
+           "moe_quantize_fp8",
+           # include/moe_balance.h
+           "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
+           # include/moe_lora.h
+           "moe_lora_linear_workspace_size", "moe_lora_linear",
+           "moe_lora_backward_workspace_size", "moe_lora_linear_backward"]
 
 
 class MoEError(RuntimeError):
@@ -76,6 +81,25 @@ def _load():
     lib.moe_combine.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp]
     lib.moe_quantize_fp8.restype = i32
     lib.moe_quantize_fp8.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    f32 = C.c_float
+    lib.moe_balance_loss_workspace_size.restype = sz
+    lib.moe_balance_loss_workspace_size.argtypes = [i32, i32, i32]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_balance_loss.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp,
+                                     sz, vp]
+    lib.moe_route_backward.restype = i32
+    lib.moe_route_backward.argtypes = [vp, vp, vp, u32, vp, vp, f32, vp, vp, vp, i32, i32, i32,
+                                       i32, vp, vp]
+    lib.moe_lora_linear_workspace_size.restype = sz
+    lib.moe_lora_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.moe_lora_linear.restype = i32
+    lib.moe_lora_linear.argtypes = [vp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp,
+                                    i32, vp, vp, sz, vp]
+    lib.moe_lora_backward_workspace_size.restype = sz
+    lib.moe_lora_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.moe_lora_linear_backward.restype = i32
+    lib.moe_lora_linear_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, i32, i32,
+                                             i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     if lib.moe_abi_version() != ABI_VERSION:
         raise ImportError("libmoe.so ABI version %d, binding expects %d"
                           % (lib.moe_abi_version(), ABI_VERSION))
@@ -338,4 +362,199 @@ def moe_quantize_fp8(src, q, scale, *, block_rows=128, block_cols=128, stream=No
     R, Cn = src.shape
     return _invoke("moe_quantize_fp8", lib.moe_quantize_fp8,
                    _ptr(src), _dt(src), R, Cn, block_rows, block_cols, _ptr(q), _ptr(scale),
+                   _stream(stream))
+
+
+# ----------------------------------------------------------------------------
+# include/moe_balance.h and include/moe_lora.h.  Every tensor is checked for
+# its type, shape, contiguity and device before the library is called.
+# ----------------------------------------------------------------------------
+
+def _arg(t, name, dtype, *shape, device):
+    """Pointer of tensor t (None: NULL), which must be a contiguous
+    dtype[shape] on the GPU `device` (an index)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor, got %r" % (name, type(t)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != device:
+        raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
+    return t.data_ptr()
+
+
+def _gpu(t, name):
+    """Index of the GPU that holds t: the current one, since a launch goes
+    there."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("%s must be on a GPU" % name)
+    if device != torch.cuda.current_device():
+        raise ValueError("%s is on GPU %d, which is not the current device" % (name, device))
+    return device
+
+
+def _pitched(W, name, dtype, rows, cols, device):
+    """(pointer, row pitch in elements) of a [rows][cols] matrix whose rows
+    may sit further apart than cols; (None, 0) for None."""
+    if W is None:
+        return None, 0
+    if not isinstance(W, torch.Tensor) or W.dtype != dtype:
+        raise TypeError("%s must be a %s tensor" % (name, dtype))
+    if W.shape != (rows, cols):
+        raise ValueError("%s must be [%d][%d], got %s" % (name, rows, cols, list(W.shape)))
+    ld = W.stride(0) if rows > 1 else cols
+    if (cols > 1 and W.stride(1) != 1) or ld < cols:
+        raise ValueError("%s must have rows of unit stride, strides %s given" % (name, W.stride()))
+    if W.get_device() != device:
+        raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
+    return W.data_ptr(), ld
+
+
+def _workspace(ws, size, device, stream):
+    """(tensor, bytes) of the workspace: ws, or a new one for this call."""
+    if ws is None:
+        if _deferring():
+            raise ValueError("a call under deferred() needs its workspace passed")
+        ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda:%d" % device)
+        if stream is not None:
+            ws.record_stream(stream)
+    elif not ws.is_contiguous() or ws.get_device() != device:
+        raise ValueError("ws must be contiguous and on GPU %d" % device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _tokens(seq_offsets, token_mask, T, device):
+    """(S, pointer of seq_offsets, pointer of token_mask)"""
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if S < 1:
+        raise ValueError("seq_offsets must hold at least two entries")
+    off = _arg(seq_offsets, "seq_offsets", torch.int32, S + 1, device=device)
+    mdt = torch.bool if token_mask is None else token_mask.dtype
+    if mdt not in (torch.bool, torch.uint8):
+        raise TypeError("token_mask must be bool or uint8, got %s" % mdt)
+    return S, off, _arg(token_mask, "token_mask", mdt, T, device=device)
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, S: int) -> int:
+    return int(lib.moe_balance_loss_workspace_size(T, E, S))
+
+
+def moe_balance_loss(logits, topk_idx, counts, probs, tokens, loss, *, alpha=0.01,
+                     seq_offsets=None, token_mask=None, ws=None, stream=None):
+    """Load-balance loss and per-expert counts of a routing decision.  logits
+    [T][E] fp32, topk_idx [T][k] int32; seq_offsets [S+1] int32 are the
+    sequences of the batch (None: one, the whole batch), token_mask [T] bool
+    or uint8 is 0 for padding.  Written: counts [S][E] int32, probs [S][E]
+    fp32, tokens [S+1] int32 (of each sequence, then the number of sequences
+    that have any) and loss [1] fp32.  ws: moe_balance_loss_workspace_size(T,
+    E, S) bytes; when None, one is allocated here for this call."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    dev = _gpu(logits, "logits")
+    S, off, mask = _tokens(seq_offsets, token_mask, T, dev)
+    i32, f32 = torch.int32, torch.float32
+    ws, ws_bytes = _workspace(ws, moe_balance_loss_workspace_size(T, E, S), dev, stream)
+    return _invoke("moe_balance_loss", lib.moe_balance_loss,
+                   _arg(logits, "logits", f32, T, E, device=dev),
+                   _arg(topk_idx, "topk_idx", i32, T, k, device=dev), off, mask, T, E, k, S,
+                   float(alpha), _arg(counts, "counts", i32, S, E, device=dev),
+                   _arg(probs, "probs", f32, S, E, device=dev),
+                   _arg(tokens, "tokens", i32, S + 1, device=dev),
+                   _arg(loss, "loss", f32, 1, device=dev), ws.data_ptr(), ws_bytes,
+                   _stream(stream))
+
+
+def moe_route_backward(logits, topk_idx, d_logits, *, d_topk_w=None, flags=0, counts=None,
+                       tokens=None, alpha=0.01, d_loss=None, seq_offsets=None, token_mask=None,
+                       stream=None):
+    """Gradient d_logits [T][E] of the router's logits: of the gate weights
+    from d_topk_w [T][k] (flags MOE_ROUTE_RENORM as in moe_route), and of the
+    balance loss from its counts and tokens and d_loss [1] (None: 1).  Either
+    term may be left out.  Tokens outside the sequences or masked get zeros."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    dev = _gpu(logits, "logits")
+    S, off, mask = _tokens(seq_offsets, token_mask, T, dev)
+    i32, f32 = torch.int32, torch.float32
+    return _invoke("moe_route_backward", lib.moe_route_backward,
+                   _arg(logits, "logits", f32, T, E, device=dev),
+                   _arg(topk_idx, "topk_idx", i32, T, k, device=dev),
+                   _arg(d_topk_w, "d_topk_w", f32, T, k, device=dev), flags,
+                   _arg(counts, "counts", i32, S, E, device=dev),
+                   _arg(tokens, "tokens", i32, S + 1, device=dev), float(alpha),
+                   _arg(d_loss, "d_loss", f32, 1, device=dev), off, mask, T, E, k, S,
+                   _arg(d_logits, "d_logits", f32, T, E, device=dev), _stream(stream))
+
+
+def _lora_dt(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise TypeError("unsupported dtype %s" % dtype)
+
+
+def moe_lora_linear_workspace_size(T: int, N: int, K: int, r: int, n: int, dtype) -> int:
+    return int(lib.moe_lora_linear_workspace_size(T, N, K, r, n, _lora_dt(dtype)))
+
+
+def moe_lora_linear(x, A, B, scale, adapter, y, v, *, W=None, ws=None, stream=None):
+    """y = x W^T + (low-rank part of each row's adapter).  x [T][K], W [N][K]
+    (rows may be padded), A [n][r][K], B [n][r][N] of one type (bf16 or fp32);
+    scale [n] fp32; adapter [T] int32, outside [0, n) for none; y [T][N] of
+    that type or fp32 and v [T][r] fp32 (for the backward pass) are written.
+    W None: the low-rank part is added to y in place.  ws:
+    moe_lora_linear_workspace_size bytes; when None, one is allocated here for
+    this call."""
+    T, K = x.shape
+    n, r, N = B.shape
+    dt, f32 = x.dtype, torch.float32
+    if y.dtype not in (dt, f32):
+        raise TypeError("y must be %s or %s, got %s" % (dt, f32, y.dtype))
+    dev = _gpu(x, "x")
+    ws, ws_bytes = _workspace(ws, moe_lora_linear_workspace_size(T, N, K, r, n, dt), dev, stream)
+    pw, ldw = _pitched(W, "W", dt, N, K, dev)
+    return _invoke("moe_lora_linear", lib.moe_lora_linear,
+                   _arg(x, "x", dt, T, K, device=dev), pw, ldw,
+                   _arg(A, "A", dt, n, r, K, device=dev), _arg(B, "B", dt, n, r, N, device=dev),
+                   _lora_dt(dt), _arg(scale, "scale", f32, n, device=dev),
+                   _arg(adapter, "adapter", torch.int32, T, device=dev), T, N, K, r, n,
+                   _arg(y, "y", y.dtype, T, N, device=dev), _lora_dt(y.dtype),
+                   _arg(v, "v", f32, T, r, device=dev), ws.data_ptr(), ws_bytes, _stream(stream))
+
+
+def moe_lora_backward_workspace_size(T: int, N: int, K: int, r: int, n: int, dtype) -> int:
+    return int(lib.moe_lora_backward_workspace_size(T, N, K, r, n, _lora_dt(dtype)))
+
+
+def moe_lora_linear_backward(dy, x, A, B, scale, adapter, v, u, *, W_t=None, dx=None, dA=None,
+                             dB=None, ws=None, stream=None):
+    """Gradients of moe_lora_linear with a frozen W: dy [T][N], x, A, B,
+    scale, adapter and v as in the forward pass; W_t [K][N] is W transposed.
+    Written: u [T][r] fp32, dx [T][K] (W_t None: the low-rank part is added to
+    dx in place) and, if given, dA [n][r][K] and dB [n][r][N] fp32.  ws:
+    moe_lora_backward_workspace_size bytes; when None, one is allocated here
+    for this call."""
+    T, N = dy.shape
+    n, r, K = A.shape
+    dt, f32 = dy.dtype, torch.float32
+    dev = _gpu(dy, "dy")
+    ws, ws_bytes = _workspace(ws, moe_lora_backward_workspace_size(T, N, K, r, n, dt), dev, stream)
+    pw, ldw = _pitched(W_t, "W_t", dt, K, N, dev)
+    return _invoke("moe_lora_linear_backward", lib.moe_lora_linear_backward,
+                   _arg(dy, "dy", dt, T, N, device=dev), _arg(x, "x", dt, T, K, device=dev), pw,
+                   ldw, _arg(A, "A", dt, n, r, K, device=dev),
+                   _arg(B, "B", dt, n, r, N, device=dev), _lora_dt(dt),
+                   _arg(scale, "scale", f32, n, device=dev),
+                   _arg(adapter, "adapter", torch.int32, T, device=dev),
+                   _arg(v, "v", f32, T, r, device=dev), T, N, K, r, n,
+                   _arg(u, "u", f32, T, r, device=dev), _arg(dx, "dx", dt, T, K, device=dev),
+                   _arg(dA, "dA", f32, n, r, K, device=dev),
+                   _arg(dB, "dB", f32, n, r, N, device=dev), ws.data_ptr(), ws_bytes,
                    _stream(stream))

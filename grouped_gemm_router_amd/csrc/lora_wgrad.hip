@@ -1,0 +1,295 @@
+// lora_wgrad.hip -- the adapters' gradients: for every adapter a,
+//   dA[a][j] = sum over its rows t of u[t][j] x[t],
+//   dB[a][j] = sum over its rows t of v[t][j] dy[t].
+//
+// The rows of an adapter may lie anywhere in the batch, so one small launch
+// sorts the rows by adapter (stably, so every sum has a fixed order) and cuts
+// each adapter's rows into units of at most TS.  The second launch is the
+// product: a workgroup takes a unit, 128 columns and 16 or 32 ranks, and its
+// four waves take 32 rows in turn.  The sum runs over rows, so a lane loads
+// 16 bytes (8 columns) of 8 rows and turns that 8 x 8 block in registers into
+// eight matrix-core fragments; x and dy are read once, in whole lines, which
+// is what bounds this (2 r flops per 2 bytes).  u and v are fp32 and enter as
+// three bf16 terms each, so no bit of them is lost.  A unit that is all of
+// its adapter writes the gradient itself; the slices of a longer one go to
+// the workspace and the third launch adds them in order (and writes zeros for
+// adapters without rows).
+#include "lora_internal.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kPlanWaves = 16;
+constexpr int kColTile = 128;
+
+// rows per unit: enough units to fill the chip, at most 64 slices to add
+int unit_rows(int T) {
+  const int by = ((T + 31) / 32 + 31) / 32 * 32;
+  return by > 256 ? by : 256;
+}
+
+struct Unit {
+  int adapter, pos, count, slot;  // slot < 0: the adapter's only unit
+};
+
+struct Ws {
+  size_t order, units, adapters, n_units, part, bytes;
+  int TS, max_units;
+};
+
+Ws layout(int T, int N, int K, int r, int n) {
+  Ws w;
+  w.TS = unit_rows(T);
+  w.max_units = T / w.TS + (n < T ? n : T);
+  // an adapter of c > TS rows has fewer than 2 c / TS units
+  const size_t slots = T <= w.TS ? 0 : 2 * (size_t)T / w.TS + 1;
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  w.order = 0;
+  w.units = up((size_t)T * 4);
+  w.adapters = w.units + up((size_t)w.max_units * sizeof(Unit));
+  w.n_units = w.adapters + up((size_t)n * 8);
+  w.part = w.n_units + 256;
+  w.bytes = w.part + slots * r * ((size_t)K + N) * 4;
+  return w;
+}
+
+// exclusive scan over the workgroup's 1024 threads; *total: the sum
+__device__ __forceinline__ int block_scan(int v, int *s_w, int *total) {
+  const int wv = threadIdx.x / kWave;
+  int sum;
+  const int ex = wave_exclusive_scan(v, &sum);
+  if (lane_id() == 0) s_w[wv] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kPlanWaves; ++w) {
+    if (w < wv) before += s_w[w];
+    all += s_w[w];
+  }
+  __syncthreads();
+  *total = all;
+  return ex + before;
+}
+
+// One workgroup.  Wave w takes the w-th sixteenth of the rows; count[w][a]
+// becomes the place of its next row of adapter a.
+__global__ __launch_bounds__(kPlanWaves *kWave) void wgrad_plan_kernel(
+    const int32_t *__restrict__ adapter, int T, int n, int TS, int32_t *__restrict__ order,
+    Unit *__restrict__ units, int2 *__restrict__ adapters, int32_t *__restrict__ n_units) {
+  __shared__ int count[kPlanWaves][MOE_LORA_MAX_ADAPTERS];
+  __shared__ int s_w[kPlanWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  for (int i = tid; i < kPlanWaves * n; i += kPlanWaves * kWave) count[i / n][i % n] = 0;
+  __syncthreads();
+  const int chunk = ((T + kPlanWaves - 1) / kPlanWaves + kWave - 1) / kWave * kWave;
+  const long long c0 = (long long)wv * chunk;
+  const int t0 = (int)min(c0, (long long)T), t1 = (int)min(c0 + chunk, (long long)T);
+  for (int t = t0 + lane; t < t1; t += kWave) {
+    const int a = adapter[t];
+    if (a >= 0 && a < n) atomicAdd(&count[wv][a], 1);
+  }
+  __syncthreads();
+  int mine = 0;
+  if (tid < n)
+    for (int w = 0; w < kPlanWaves; ++w) mine += count[w][tid];
+  const int nu = (mine + TS - 1) / TS;
+  int rows_all, units_all, slots_all;
+  const int pos = block_scan(mine, s_w, &rows_all);
+  const int u0 = block_scan(nu, s_w, &units_all);
+  const int slot0 = block_scan(nu > 1 ? nu : 0, s_w, &slots_all);
+  if (tid < n) {
+    int at = pos;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int c = count[w][tid];
+      count[w][tid] = at;
+      at += c;
+    }
+    adapters[tid] = make_int2(slot0, nu);
+    for (int i = 0; i < nu; ++i)
+      units[u0 + i] = Unit{tid, pos + i * TS, min(TS, mine - i * TS), nu > 1 ? slot0 + i : -1};
+  }
+  if (tid == 0) *n_units = units_all;
+  __syncthreads();
+  // this wave's row of count only, lane to lane: volatile, so that every turn
+  // reads what the turn before stored
+  volatile int *next = count[wv];
+  for (int b = t0; b < t1; b += kWave) {
+    const int t = b + lane;
+    int a = t < t1 ? adapter[t] : -1;
+    if (a < 0 || a >= n) a = -1;
+    unsigned long long todo = __ballot(a >= 0);
+    while (todo) {  // one turn per adapter among these 64 rows
+      const int first = __builtin_ctzll(todo);
+      const int who = __builtin_amdgcn_readlane(a, first);
+      const unsigned long long same = __ballot(a == who);
+      const int at = next[who];
+      if (a == who) order[at + __popcll(same & ((1ull << lane) - 1))] = t;
+      if (lane == first) next[who] = at + __popcll(same);
+      todo &= ~same;
+    }
+  }
+}
+
+// grid (units, column tiles of x then of dy, rank groups of 16 NR)
+template <int ES, int NR>
+__global__ __launch_bounds__(256) void wgrad_kernel(
+    const char *__restrict__ x, const char *__restrict__ dy, const float *__restrict__ u,
+    const float *__restrict__ v, const int32_t *__restrict__ order, const Unit *__restrict__ units,
+    const int32_t *__restrict__ n_units, int N, int K, int r, float *__restrict__ dA,
+    float *__restrict__ dB, float *__restrict__ part) {
+  __shared__ float red[4][16][kColTile + 4];
+  if ((int)blockIdx.x >= *n_units) return;
+  const Unit un = units[blockIdx.x];
+  const int ka = (K + kColTile - 1) / kColTile;
+  const bool is_a = (int)blockIdx.y < ka;
+  const int C = is_a ? K : N, c0 = (is_a ? blockIdx.y : blockIdx.y - ka) * kColTile;
+  const int j0 = blockIdx.z * 16 * NR;
+  const char *q = is_a ? x : dy;
+  const float *p = is_a ? u : v;
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  const int fr = lane & 15, fq = lane >> 4;
+  const int col = c0 + 8 * fr;
+  const bool in_c = col < C;  // C is a multiple of 8
+  f32x4 acc[NR][8];
+#pragma unroll
+  for (int b = 0; b < NR; ++b)
+#pragma unroll
+    for (int f = 0; f < 8; ++f) acc[b][f] = f32x4{};
+
+  for (int s = wv * 32; s < un.count; s += 4 * 32) {
+    // rows past the unit's end read as zero in both operands
+    int id[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = s + fq * 8 + i;
+      id[i] = k < un.count ? order[un.pos + k] : -1;
+    }
+    u32x4 qv[8][ES / 2];
+    float pv[NR][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = id[i] >= 0;
+      const size_t t = in ? id[i] : 0;
+#pragma unroll
+      for (int h = 0; h < ES / 2; ++h)
+        qv[i][h] = in && in_c ? *reinterpret_cast<const u32x4 *>(q + (t * C + col) * ES + 16 * h)
+                              : u32x4{};
+#pragma unroll
+      for (int b = 0; b < NR; ++b) {
+        const int j = j0 + b * 16 + fr;
+        pv[b][i] = in && j < r ? p[t * r + j] : 0.f;
+      }
+    }
+    if constexpr (ES == 2) {
+      bf16x8 pt[NR][3];
+#pragma unroll
+      for (int b = 0; b < NR; ++b) split_bf16<3>(pv[b], pt[b]);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+        // column f of the lane's 8 x 8 block: row pairs into words
+        const unsigned sel = (f & 1) ? 0x07060302u : 0x05040100u;
+        u32x4 w;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          w[d] = __builtin_amdgcn_perm(qv[2 * d + 1][0][f >> 1], qv[2 * d][0][f >> 1], sel);
+        const bf16x8 qf = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+        for (int b = 0; b < NR; ++b)
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            acc[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pt[b][k], qf, acc[b][f], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+#pragma unroll
+          for (int b = 0; b < NR; ++b)
+            acc[b][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                pv[b][i], __uint_as_float(qv[i][f >> 2 & (ES / 2 - 1)][f & 3]), acc[b][f], 0, 0, 0);
+    }
+  }
+  // the four waves' sums, in wave order
+  const int width = un.slot < 0 ? C : K + N;
+  float *out = un.slot < 0 ? (is_a ? dA : dB) + (size_t)un.adapter * r * C + c0
+                           : part + (size_t)un.slot * r * width + (is_a ? c0 : K + c0);
+#pragma unroll
+  for (int b = 0; b < NR; ++b) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int f = 0; f < 8; ++f) red[wv][4 * fq + i][8 * fr + f] = acc[b][f][i];
+    __syncthreads();
+    for (int e = tid; e < 16 * kColTile / 4; e += 256) {
+      const int jr = e / (kColTile / 4), c = (e % (kColTile / 4)) * 4, j = j0 + b * 16 + jr;
+      if (j >= r || c0 + c >= C) continue;
+      f32x4 sum = *reinterpret_cast<const f32x4 *>(&red[0][jr][c]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) sum += *reinterpret_cast<const f32x4 *>(&red[w][jr][c]);
+      *reinterpret_cast<f32x4 *>(out + (size_t)j * width + c) = sum;
+    }
+  }
+}
+
+// grid (pieces of r (K + N) / 4, adapters)
+__global__ __launch_bounds__(256) void wgrad_reduce_kernel(const int2 *__restrict__ adapters,
+                                                           const float *__restrict__ part, int N,
+                                                           int K, int r, float *__restrict__ dA,
+                                                           float *__restrict__ dB) {
+  const int a = blockIdx.y;
+  const int2 s = adapters[a];
+  if (s.y == 1) return;
+  const int wide = (K + N) / 4;
+  const long long q = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (q >= (long long)r * wide) return;
+  const int j = (int)(q / wide), c = (int)(q - (long long)j * wide) * 4;
+  f32x4 sum = f32x4{};
+  const float *src = part + (size_t)s.x * r * (K + N) + (size_t)j * (K + N) + c;
+  for (int i = 0; i < s.y; ++i)
+    sum += *reinterpret_cast<const f32x4 *>(src + (size_t)i * r * (K + N));
+  float *out = c < K ? dA + ((size_t)a * r + j) * K + c : dB + ((size_t)a * r + j) * N + (c - K);
+  *reinterpret_cast<f32x4 *>(out) = sum;
+}
+
+template <int ES>
+void launch_t(const void *dy, const void *x, const float *u, const float *v, const Ws &w, char *ws,
+              int N, int K, int r, float *dA, float *dB, hipStream_t s) {
+  const int cols = (K + kColTile - 1) / kColTile + (N + kColTile - 1) / kColTile;
+  const int32_t *order = reinterpret_cast<const int32_t *>(ws + w.order);
+  const Unit *units = reinterpret_cast<const Unit *>(ws + w.units);
+  const int32_t *nu = reinterpret_cast<const int32_t *>(ws + w.n_units);
+  float *part = reinterpret_cast<float *>(ws + w.part);
+  const char *xb = static_cast<const char *>(x), *db = static_cast<const char *>(dy);
+  if (r <= 16)
+    hipLaunchKernelGGL((wgrad_kernel<ES, 1>), dim3(w.max_units, cols, 1), dim3(256), 0, s, xb, db, u,
+                       v, order, units, nu, N, K, r, dA, dB, part);
+  else
+    hipLaunchKernelGGL((wgrad_kernel<ES, 2>), dim3(w.max_units, cols, (r + 31) / 32), dim3(256), 0, s,
+                       xb, db, u, v, order, units, nu, N, K, r, dA, dB, part);
+}
+
+}  // namespace
+
+size_t lora_wgrad_ws_bytes(int T, int N, int K, int r, int n) { return layout(T, N, K, r, n).bytes; }
+
+hipError_t launch_lora_wgrad(const void *dy, const void *x, int dt, const float *u, const float *v,
+                             const int32_t *adapter, int T, int N, int K, int r, int n, float *dA,
+                             float *dB, void *ws, hipStream_t s) {
+  const Ws w = layout(T, N, K, r, n);
+  char *b = static_cast<char *>(ws);
+  hipLaunchKernelGGL(wgrad_plan_kernel, dim3(1), dim3(kPlanWaves * kWave), 0, s, adapter, T, n, w.TS,
+                     reinterpret_cast<int32_t *>(b + w.order), reinterpret_cast<Unit *>(b + w.units),
+                     reinterpret_cast<int2 *>(b + w.adapters),
+                     reinterpret_cast<int32_t *>(b + w.n_units));
+  if (T > 0) {
+    if (dt == MOE_BF16) launch_t<2>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
+    else launch_t<4>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
+  }
+  const long long pieces = (long long)r * ((K + N) / 4);
+  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)((pieces + 255) / 256), n), dim3(256), 0, s,
+                     reinterpret_cast<const int2 *>(b + w.adapters),
+                     reinterpret_cast<const float *>(b + w.part), N, K, r, dA, dB);
+  return hipGetLastError();
+}

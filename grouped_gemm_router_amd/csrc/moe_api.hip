@@ -1,12 +1,15 @@
 // moe_api.hip -- the extern "C" entry points of libmoe.so (declared and
-// documented in include/moe.h).  Each entry point checks its arguments on
-// the host, returns a status without launching anything if they are bad,
-// and otherwise enqueues the kernels on the caller's stream.  Nothing here
-// allocates, frees, synchronises or reads device memory.
+// documented in include/moe.h, moe_balance.h and moe_lora.h).  Each entry
+// point checks its arguments on the host, returns a status without launching
+// anything if they are bad, and otherwise enqueues the kernels on the
+// caller's stream.  Nothing here allocates, frees, synchronises or reads
+// device memory.
 #include <stdint.h>
 
 #include <atomic>
 
+#include "../../include/moe_balance.h"
+#include "lora_internal.h"
 #include "moe_internal.h"
 
 namespace {
@@ -285,6 +288,163 @@ moe_status_t moe_quantize_fp8(const void *src, moe_dtype_t src_dt, int R, int C,
   if (R == 0 || C == 0) return MOE_OK;
   return launched(launch_quantize_fp8(src, src_dt, R, C, block_rows, block_cols, q, scale,
                                       as_stream(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// moe_balance.h
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// sizes, sequences and mask that both balance entries take
+moe_status_t balance_sizes(const int32_t *seq_offsets, int T, int E, int k, int S) {
+  if (T < 0 || E < 1 || k < 1 || k > E || S < 1) return MOE_ERR_INVALID;
+  if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
+  // (a launch has fewer than 2^32 threads)
+  if (T > (1 << 26)) return MOE_ERR_UNSUPPORTED;
+  if (S > 1 && !seq_offsets) return MOE_ERR_INVALID;
+  if (!opt_aligned4(seq_offsets)) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_balance_loss_workspace_size(int T, int E, int S) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || S < 1 || S > MOE_MAX_SEQUENCES) return 0;
+  return balance_loss_ws_bytes(T, E, S);
+}
+
+moe_status_t moe_balance_loss(const float *logits, const int32_t *topk_idx,
+                              const int32_t *seq_offsets, const uint8_t *token_mask, int T,
+                              int E, int k, int S, float alpha, int32_t *counts, float *probs,
+                              int32_t *tokens, float *loss, void *ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+  const moe_status_t sizes = balance_sizes(seq_offsets, T, E, k, S);
+  if (sizes != MOE_OK) return sizes;
+  if (T > 0 && (!aligned16(logits) || !aligned4(topk_idx))) return MOE_ERR_INVALID;
+  if (!aligned4(counts) || !aligned4(probs) || !aligned4(tokens) || !aligned4(loss))
+    return MOE_ERR_INVALID;
+  if (ws_bytes < balance_loss_ws_bytes(T, E, S)) return MOE_ERR_WORKSPACE;
+  if (!aligned4(ws)) return MOE_ERR_INVALID;
+  return launched(launch_balance_loss(logits, topk_idx, seq_offsets, token_mask, T, E, k, S, alpha,
+                                      counts, probs, tokens, loss, ws, as_stream(stream)));
+}
+
+moe_status_t moe_route_backward(const float *logits, const int32_t *topk_idx,
+                                const float *d_topk_w, unsigned flags, const int32_t *counts,
+                                const int32_t *tokens, float alpha, const float *d_loss,
+                                const int32_t *seq_offsets, const uint8_t *token_mask, int T,
+                                int E, int k, int S, float *d_logits, moe_stream_t stream) {
+  const moe_status_t sizes = balance_sizes(seq_offsets, T, E, k, S);
+  if (sizes != MOE_OK) return sizes;
+  if (flags & ~MOE_ROUTE_RENORM) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!aligned16(logits) || !aligned16(d_logits) || !aligned4(topk_idx) ||
+      !opt_aligned4(d_topk_w) || !opt_aligned4(counts) || !opt_aligned4(tokens) ||
+      !opt_aligned4(d_loss))
+    return MOE_ERR_INVALID;
+  if ((counts == nullptr) != (tokens == nullptr)) return MOE_ERR_INVALID;
+  if (!d_topk_w && (!counts || flags != 0)) return MOE_ERR_INVALID;
+  if (d_loss && !counts) return MOE_ERR_INVALID;
+  if (d_logits == logits) return MOE_ERR_INVALID;
+  return launched(launch_route_backward(logits, topk_idx, d_topk_w, (flags & MOE_ROUTE_RENORM) != 0,
+                                        counts, tokens, alpha, d_loss, seq_offsets, token_mask, T, E,
+                                        k, S, d_logits, as_stream(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// moe_lora.h
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// the sizes of both lora entries
+moe_status_t lora_sizes(int T, int N, int K, int r, int n, moe_dtype_t dt) {
+  if (T < 0 || N < 1 || K < 1 || r < 1 || n < 1) return MOE_ERR_INVALID;
+  if (!is_act(dt)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 != 0 || r % 8 != 0 || r > MOE_LORA_MAX_RANK || n > MOE_LORA_MAX_ADAPTERS)
+    return MOE_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 128 x 128
+  if (T > (1 << 24) || N > (1 << 20) || K > (1 << 20) ||
+      (long long)T * (N > K ? N : K) > (1ll << 36))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// a row pitch of the shared weights (0: dense)
+bool pitch_ok(int *ld, int row, moe_dtype_t dt, const void *w) {
+  if (!w) return *ld == 0;
+  if (*ld == 0) *ld = row;
+  return *ld >= row && (long long)*ld * (dt == MOE_BF16 ? 2 : 4) % 16 == 0 && aligned16(w);
+}
+
+}  // namespace
+
+size_t moe_lora_linear_workspace_size(int T, int N, int K, int r, int n, moe_dtype_t dt) {
+  (void)T, (void)N, (void)K, (void)r, (void)n, (void)dt;
+  return 0;
+}
+
+moe_status_t moe_lora_linear(const void *x, const void *W, int ldw, const void *A,
+                             const void *B, moe_dtype_t dt, const float *scale,
+                             const int32_t *adapter, int T, int N, int K, int r, int n, void *y,
+                             moe_dtype_t y_dt, float *v, void *ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  const moe_status_t sizes = lora_sizes(T, N, K, r, n, dt);
+  if (sizes != MOE_OK) return sizes;
+  if (!is_act(y_dt) || (dt == MOE_F32 && y_dt != MOE_F32)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(y) || !aligned16(v) ||
+      !aligned4(scale) || !aligned4(adapter) || !pitch_ok(&ldw, K, dt, W))
+    return MOE_ERR_INVALID;
+  if (ws == nullptr && ws_bytes != 0) return MOE_ERR_INVALID;
+  if (ws_bytes < moe_lora_linear_workspace_size(T, N, K, r, n, dt)) return MOE_ERR_WORKSPACE;
+  const hipStream_t s = as_stream(stream);
+  const hipError_t e = launch_lora_shrink(x, A, dt, scale, adapter, T, K, r, n, v, s);
+  if (e != hipSuccess) return launched(e);
+  return launched(launch_lora_expand(x, W, ldw, B, dt, v, adapter, T, N, K, r, n, y, y_dt,
+                                     current_device_cus(), s));
+}
+
+size_t moe_lora_backward_workspace_size(int T, int N, int K, int r, int n, moe_dtype_t dt) {
+  if (lora_sizes(T, N, K, r, n, dt) != MOE_OK || N % 8 != 0) return 0;
+  return lora_wgrad_ws_bytes(T, N, K, r, n);
+}
+
+moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void *W_t, int ldw,
+                                      const void *A, const void *B, moe_dtype_t dt,
+                                      const float *scale, const int32_t *adapter,
+                                      const float *v, int T, int N, int K, int r, int n,
+                                      float *u, void *dx, float *dA, float *dB, void *ws,
+                                      size_t ws_bytes, moe_stream_t stream) {
+  const moe_status_t sizes = lora_sizes(T, N, K, r, n, dt);
+  if (sizes != MOE_OK) return sizes;
+  if (N % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((dA == nullptr) != (dB == nullptr) || (!dx && !dA)) return MOE_ERR_INVALID;
+  if (dA) {
+    if (!aligned16(dA) || !aligned16(dB)) return MOE_ERR_INVALID;
+    if (ws_bytes < lora_wgrad_ws_bytes(T, N, K, r, n)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_INVALID;
+  }
+  if (T == 0) {  // no row of any adapter: zeros
+    if (!dA) return MOE_OK;
+    return launched(launch_lora_wgrad(dy, x, dt, u, v, adapter, T, N, K, r, n, dA, dB, ws,
+                                      as_stream(stream)));
+  }
+  if (!aligned16(dy) || !aligned16(A) || !aligned16(B) || !aligned16(u) || !aligned4(scale) ||
+      !aligned4(adapter))
+    return MOE_ERR_INVALID;
+  if (dx ? !aligned16(dx) || !pitch_ok(&ldw, N, dt, W_t) : W_t != nullptr || ldw != 0)
+    return MOE_ERR_INVALID;
+  if (dA && (!aligned16(x) || !aligned16(v))) return MOE_ERR_INVALID;
+  const hipStream_t s = as_stream(stream);
+  hipError_t e = launch_lora_shrink(dy, B, dt, scale, adapter, T, N, r, n, u, s);
+  if (e == hipSuccess && dx)
+    e = launch_lora_expand(dy, W_t, ldw, A, dt, u, adapter, T, K, N, r, n, dx, dt,
+                           current_device_cus(), s);
+  if (e == hipSuccess && dA)
+    e = launch_lora_wgrad(dy, x, dt, u, v, adapter, T, N, K, r, n, dA, dB, ws, s);
+  return launched(e);
 }
 
 }  // extern "C"

@@ -201,6 +201,41 @@ class MoELayer:
         return {"f": f, "P": P, "aux_loss": summary[0], "max_over_mean": summary[1],
                 "entropy_bits": summary[2]}
 
+    def balance_loss(self, alpha: float = 0.01, *, seq_offsets=None, token_mask=None):
+        """Balance loss and per-expert counts of the last forward's routing
+        (needs keep_logits): a dict of loss [1], counts [S][E], probs [S][E]
+        and tokens [S+1] device tensors, over the sequences and the mask of
+        moe_balance_loss.  Enqueued on the current stream."""
+        if self.logits is None:
+            raise RuntimeError("balance_loss needs the logits: build the layer with "
+                               "keep_logits=True")
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        i32, f32, dev = torch.int32, torch.float32, self.device
+        out = {"loss": torch.empty((1,), dtype=f32, device=dev),
+               "counts": torch.empty((S, self.E), dtype=i32, device=dev),
+               "probs": torch.empty((S, self.E), dtype=f32, device=dev),
+               "tokens": torch.empty((S + 1,), dtype=i32, device=dev)}
+        api.moe_balance_loss(self.logits, self.topk_idx, out["counts"], out["probs"],
+                             out["tokens"], out["loss"], alpha=alpha, seq_offsets=seq_offsets,
+                             token_mask=token_mask)
+        return out
+
+    def route_backward(self, d_topk_w=None, *, balance=None, d_loss=None, alpha: float = 0.01,
+                       seq_offsets=None, token_mask=None):
+        """Gradient [T][E] of the last forward's router logits: of its gate
+        weights from d_topk_w [T][k], and of a balance_loss() result (same
+        alpha, sequences and mask) from d_loss [1] (None: 1)."""
+        if self.logits is None:
+            raise RuntimeError("route_backward needs the logits: build the layer with "
+                               "keep_logits=True")
+        d_logits = torch.empty_like(self.logits)
+        api.moe_route_backward(self.logits, self.topk_idx, d_logits, d_topk_w=d_topk_w,
+                               flags=self.flags if d_topk_w is not None else 0,
+                               counts=balance["counts"] if balance else None,
+                               tokens=balance["tokens"] if balance else None, alpha=alpha,
+                               d_loss=d_loss, seq_offsets=seq_offsets, token_mask=token_mask)
+        return d_logits
+
     def capture(self, x, out):
         """A HIP graph (torch.cuda.CUDAGraph) of the five calls on x -> out,
         for callers that run the same shapes again and again: one replay
