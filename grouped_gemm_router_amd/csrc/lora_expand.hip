@@ -12,13 +12,12 @@
 // reads its own adapter's rows of F on the vector ALUs.  No row ever meets
 // another adapter's values, not even multiplied by zero: an infinity in one
 // request's adapter stays in that request's rows.
+#include "gemm_bf16_tile.h"
 #include "lora_internal.h"
 
 namespace {
 
 using namespace moe;
-
-__device__ __forceinline__ int swz(int row, int p) { return p ^ ((row >> 1) & 7); }
 
 // element i of a factor or of y as fp32
 template <int ES>
@@ -27,36 +26,42 @@ __device__ __forceinline__ float ld1(const char *p, size_t i) {
   else return reinterpret_cast<const float *>(p)[i];
 }
 
-// eight consecutive elements; vec: the address is 16-byte aligned and all
-// eight exist, else the first `have` exist
-template <int ES>
-__device__ __forceinline__ void ld8(const char *p, size_t i, bool vec, int have, float (&f)[8]) {
-  if (vec) {
-    if constexpr (ES == 2) {
-      const u32x4 q = *reinterpret_cast<const u32x4 *>(p + i * 2);
+// Eight consecutive elements as they are stored.  VEC: 16-byte loads of all
+// eight (the address is aligned and they exist); otherwise the first `have`
+// exist and the others repeat the last of them.  No load is under a
+// condition, so the loads of a batch are in flight together.
+template <int ES, bool VEC>
+struct Raw8 {
+  u32x4 q[ES / 2];
+  uint16_t h[VEC ? 1 : 8];
+  float s[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const char *p, size_t i, int have) {
+    if constexpr (VEC) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f[2 * c] = bf16_bits_to_f32(q[c] & 0xffffu);
-        f[2 * c + 1] = __uint_as_float(q[c] & 0xffff0000u);
-      }
+      for (int k = 0; k < ES / 2; ++k) q[k] = *reinterpret_cast<const u32x4 *>(p + i * ES + 16 * k);
     } else {
-      const f32x4 q0 = *reinterpret_cast<const f32x4 *>(p + i * 4);
-      const f32x4 q1 = *reinterpret_cast<const f32x4 *>(p + i * 4 + 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f[c] = q0[c];
-        f[4 + c] = q1[c];
+      for (int c = 0; c < 8; ++c) {
+        if constexpr (ES == 2) h[c] = reinterpret_cast<const uint16_t *>(p)[i + min(c, have - 1)];
+        else s[c] = reinterpret_cast<const float *>(p)[i + min(c, have - 1)];
       }
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] = c < have ? ld1<ES>(p, i + c) : 0.f;
   }
-}
+  __device__ __forceinline__ float get(int c) const {
+    if constexpr (VEC && ES == 2)
+      return c & 1 ? __uint_as_float(q[0][c >> 1] & 0xffff0000u) : bf16_bits_to_f32(q[0][c >> 1] & 0xffffu);
+    else if constexpr (VEC)
+      return __uint_as_float(q[(c >> 2) & (ES / 2 - 1)][c & 3]);
+    else if constexpr (ES == 2)
+      return bf16_bits_to_f32(h[c]);
+    else
+      return s[c];
+  }
+};
 
-template <int OS>
-__device__ __forceinline__ void st8(char *p, size_t i, bool vec, int have, const float (&f)[8]) {
-  if (vec) {
+template <int OS, bool VEC>
+__device__ __forceinline__ void st8(char *p, size_t i, int have, const float (&f)[8]) {
+  if constexpr (VEC) {
     if constexpr (OS == 2) {
       bf16x8 q;
 #pragma unroll
@@ -76,55 +81,79 @@ __device__ __forceinline__ void st8(char *p, size_t i, bool vec, int have, const
   }
 }
 
-// f[0..7] += sum_j vr[j] F[j][n .. n + 7] for one row's adapter
-template <int ES>
-__device__ __forceinline__ void add_low_rank(float (&f)[8], const float *vr, const char *F, int r,
-                                             int N, int n, bool vec, int have) {
-  for (int j0 = 0; j0 < r; j0 += 8) {
-    float w[8][8];
-    const f32x4 v0 = *reinterpret_cast<const f32x4 *>(vr + j0);
-    const f32x4 v1 = *reinterpret_cast<const f32x4 *>(vr + j0 + 4);
+// Eight ranks of the factor at F (rows of N) for each of the lane's columns.
+template <int NB>
+__device__ __forceinline__ void load_ranks(uint16_t (&w)[NB][8], const uint16_t *F, int N,
+                                           const int (&n)[NB]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ld8<ES>(F, (size_t)(j0 + j) * N + n, vec, have, w[j]);
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) f[c] = fmaf(j < 4 ? v0[j & 3] : v1[j & 3], w[j][c], f[c]);
-  }
+    for (int i = 0; i < 8; ++i) w[nb][i] = F[(size_t)i * N + n[nb]];
 }
 
-// acc[nb] += v F over one 32-row block that belongs to adapter a: 16 ranks a
-// step.  t: the lane's row, n[nb]: its columns.
-template <int TERMS, int NB>
-__device__ __forceinline__ void mma_low_rank(f32x16 (&acc)[NB], const float *v, const char *F, int r,
-                                             int N, size_t t, const int (&n)[NB], int fh) {
-  for (int j0 = 0; j0 < r; j0 += 16) {
-    const int j = j0 + 8 * fh;
-    const bool in = j < r;  // r is a multiple of 8: a lane's eight ranks exist or not
-    float f[8];
-    const f32x4 v0 = in ? *reinterpret_cast<const f32x4 *>(v + t * r + j) : f32x4{};
-    const f32x4 v1 = in ? *reinterpret_cast<const f32x4 *>(v + t * r + j + 4) : f32x4{};
+// The low-rank part of a wave's MI x NB blocks, for the row blocks whose 32
+// rows share an adapter: acc[i][nb] += v F, 16 ranks a step; s_hom says which
+// blocks do.  s_ad: the tile's adapters (-1 for none); first: the wave's first
+// row block; n0: its first column.
+template <int TERMS, int MI, int NB>
+__device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int *s_ad, int *s_hom,
+                                                int first, bool tell, int m0, int n0, const char *F,
+                                                const float *v, int T, int N, int r, int fr, int fh) {
+  int a[MI];
+  bool hom[MI], any = false;
+  const float *vr[MI];
+  int n[NB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = v0[i];
-      f[4 + i] = v1[i];
+  for (int j = 0; j < NB; ++j) n[j] = min(n0 + j * 32 + fr, N - 1);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int row = (first + i) * 32 + fr, mine = s_ad[row];
+    const int a0 = __builtin_amdgcn_readfirstlane(mine);
+    hom[i] = a0 >= 0 && __all(mine == a0);
+    a[i] = max(a0, 0);
+    vr[i] = v + (size_t)min(m0 + row, T - 1) * r;
+    any = any || hom[i];
+    if (tell) s_hom[first + i] = hom[i];
+  }
+  if (!any) return;
+  const uint16_t *Fw = reinterpret_cast<const uint16_t *>(F);
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    // r is a multiple of 8: a lane's eight ranks exist or not.  Where they
+    // do not, the last eight are loaded and both operands are zero.
+    const bool in = j0 + 8 * fh < r;
+    const int j = min(j0 + 8 * fh, r - 8);
+    f32x4 v0[MI], v1[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      v0[i] = *reinterpret_cast<const f32x4 *>(vr[i] + j);
+      v1[i] = *reinterpret_cast<const f32x4 *>(vr[i] + j + 4);
     }
     uint16_t w[NB][8];
+    load_ranks<NB>(w, Fw + ((size_t)a[0] * r + j) * N, N, n);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int i = 0; i < MI; ++i) {
+      // the rows of a prompt share the factor's fragments from block to block
+      if (i > 0 && a[i] != a[i - 1]) load_ranks<NB>(w, Fw + ((size_t)a[i] * r + j) * N, N, n);
+      if (!hom[i]) continue;
+      float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[nb][i] = in ? reinterpret_cast<const uint16_t *>(F)[(size_t)(j + i) * N + n[nb]] : 0;
-    bf16x8 va[TERMS];
-    split_bf16<TERMS>(f, va);
+      for (int c = 0; c < 4; ++c) {
+        f[c] = in ? v0[i][c] : 0.f;
+        f[4 + c] = in ? v1[i][c] : 0.f;
+      }
+      bf16x8 va[TERMS];
+      split_bf16<TERMS>(f, va);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      bf16x8 b;
+      for (int nb = 0; nb < NB; ++nb) {
+        u32x4 q;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = __builtin_bit_cast(__bf16, w[nb][i]);
+        for (int c = 0; c < 4; ++c)
+          q[c] = in ? (uint32_t)w[nb][2 * c] | ((uint32_t)w[nb][2 * c + 1] << 16) : 0u;
+        const bf16x8 b = __builtin_bit_cast(bf16x8, q);
 #pragma unroll
-      for (int k = 0; k < TERMS; ++k)
-        acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[k], b, acc[nb], 0, 0, 0);
+        for (int k = 0; k < TERMS; ++k)
+          acc[i][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[k], b, acc[i][nb], 0, 0, 0);
+      }
     }
   }
 }
@@ -146,29 +175,212 @@ unsigned tile_grid(int MT, int NT) {
   return (unsigned)((major + 7) / 8 * 8) * (unsigned)minor;
 }
 
+// rows [32 blk, 32 blk + 32) of a tile, staged in fp32 with row pitch SP, for
+// WM row blocks at once (stage_of(w) holds tile row block first + w * stride):
+// add what is left of the low-rank part and of y, round, store 8-column pieces
+template <int ES, int OS, int BN, int SP, int WM, bool VEC, class StageOf>
+__device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int stride, int m0,
+                                              int n0, const int *s_ad, const int *s_hom, bool add_y,
+                                              const char *F, const float *v, int T, int N, int r,
+                                              char *y) {
+  constexpr int CG = BN / 8, P = 1;  // pieces that a thread has in hand at once
+  const int nt = blockDim.x;
+  for (int q0 = threadIdx.x; q0 < WM * 32 * CG; q0 += P * nt) {
+    float f[P][8];
+    bool live[P], low[P];
+    int have[P];
+    size_t at[P];
+    const float *vr[P];
+    const char *Fp[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int q = min(q0 + p * nt, WM * 32 * CG - 1);
+      const int w = q / (32 * CG), rr = (q / CG) % 32, c = (q % CG) * 8;
+      const int blk = first + w * stride, row = blk * 32 + rr, t = m0 + row, col = n0 + c;
+      live[p] = q0 + p * nt < WM * 32 * CG && t < T && col < N;
+      const int tc = min(t, T - 1), cc = live[p] ? col : 0;  // addresses that exist
+      have[p] = N - cc;
+      at[p] = (size_t)tc * N + cc;
+      const int a = s_ad[row];
+      low[p] = live[p] && a >= 0 && !s_hom[blk];
+      vr[p] = v + (size_t)tc * r;
+      Fp[p] = F + ((size_t)max(a, 0) * r * N + cc) * ES;
+      const float *st = stage_of(w) + rr * SP + c;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[p][i] = st[i];
+    }
+    if (low[0] || low[P - 1]) {
+      // 16 ranks a step, all loads of a step before its first product; a
+      // piece without a low-rank part loads an adapter's rows and drops them
+      float g[P][8];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[p][i] = f[p][i];
+      for (int j0 = 0; j0 < r; j0 += 16) {
+        Raw8<ES, VEC> w[P][16];
+        f32x4 vv[P][4];
+        const int j8 = min(j0 + 8, r - 8);  // (r % 16 == 8: loaded again, not used)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[p][j].load(Fp[p], (size_t)(j < 8 ? j0 + j : j8 + j - 8) * N, have[p]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            vv[p][j] = *reinterpret_cast<const f32x4 *>(vr[p] + (j < 2 ? j0 : j8 - 8) + 4 * j);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && j0 + 8 >= r) break;
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 8 * h; j < 8 * h + 8; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                g[p][i] = fmaf(vv[p][j >> 2][j & 3], w[p][j].get(i), g[p][i]);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[p][i] = low[p] ? g[p][i] : f[p][i];
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (!live[p]) continue;
+      if (add_y) {
+        Raw8<OS, VEC> old;
+        old.load(y, at[p], have[p]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[p][i] += old.get(i);
+      }
+      st8<OS, VEC>(y, at[p], have[p], f[p]);
+    }
+  }
+}
+
+template <int ES, int OS, int BN, int SP, int WM, class StageOf>
+__device__ __forceinline__ void finish_rows(StageOf stage_of, int first, int stride, int m0, int n0,
+                                            const int *s_ad, const int *s_hom, bool add_y,
+                                            const char *F, const float *v, int T, int N, int r,
+                                            char *y) {
+  if (N % 8 == 0)  // rows of F and of y are then 16-byte aligned
+    finish_pieces<ES, OS, BN, SP, WM, true>(stage_of, first, stride, m0, n0, s_ad, s_hom, add_y, F, v,
+                                            T, N, r, y);
+  else
+    finish_pieces<ES, OS, BN, SP, WM, false>(stage_of, first, stride, m0, n0, s_ad, s_hom, add_y, F,
+                                             v, T, N, r, y);
+}
+
 // ---------------------------------------------------------------------------
-// tiles of BM x BN on 4 waves (WM x WN), operands through LDS 128 bytes of a
-// row at a time: the next step's pieces are loaded into registers while this
-// step is multiplied.  Pieces past K read as zero; rows past T and columns
-// past N repeat the last one and are not stored.
+// fp32: tiles of 64 x 64 on 4 waves of 32 x 32, operands through LDS 128
+// bytes of a row at a time: the next step's pieces are loaded into registers
+// while this step is multiplied.  Pieces past K read as zero; rows past T and
+// columns past N repeat the last one and are not stored.  Every row's
+// low-rank part runs on the vector ALUs in fp32.
 // ---------------------------------------------------------------------------
-template <int ES, int OS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256) void expand_tile_kernel(
+__global__ __launch_bounds__(256) void expand_f32_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
     const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
     int n, char *__restrict__ y, int MT, int NT) {
-  constexpr int MI = BM / WM / 32, NB = BN / WN / 32;
-  constexpr int NLD = (BM + BN) * 8 / 256;
-  constexpr int SP = BN + 4;  // row pitch of the staged fp32 tile
-  constexpr int RING = 2 * (BM + BN) * 128, STAGE = BM * SP * 4;
-  static_assert(WM * WN == 4 && MI >= 1 && NB >= 1, "four waves of 32 x 32 blocks");
-  __shared__ __align__(16) char smem[RING > STAGE ? RING : STAGE];
+  constexpr int BM = 64, BNF = 64, SP = BNF + 4, NLD = (BM + BNF) * 8 / 256;
+  __shared__ u32x4 ring[2][(BM + BNF) * 8];
   __shared__ int s_ad[BM];
   __shared__ int s_hom[BM / 32];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
-  const int m0 = at.mt * BM, n0 = at.nt * BN;
+  const int m0 = at.mt * BM, n0 = at.nt * BNF;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  const int wm = wv / 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
+  if (tid < BM) {
+    const int a = adapter[min(m0 + tid, T - 1)];
+    s_ad[tid] = a >= 0 && a < n ? a : -1;
+  }
+  if (tid < BM / 32) s_hom[tid] = 0;
+  f32x16 acc = f32x16{};
+  if (W) {
+    const int KP = K / 4, KT = (KP + 7) / 8;
+    const u32x4 *src[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int row = (tid + 256 * i) >> 3;
+      src[i] = row < BM
+                   ? reinterpret_cast<const u32x4 *>(x + (size_t)min(m0 + row, T - 1) * K * 4)
+                   : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * 4);
+    }
+    u32x4 reg[NLD];
+    auto fetch = [&](int kt) {
+#pragma unroll
+      for (int i = 0; i < NLD; ++i) {
+        const int p = kt * 8 + (tid & 7);
+        reg[i] = load_piece(src[i], p, KP);
+      }
+    };
+    auto put = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < NLD; ++i) {
+        const int row = (tid + 256 * i) >> 3;
+        ring[b][row * 8 + swzb(row, tid & 7)] = reg[i];
+      }
+    };
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int kt = 0; kt < KT; ++kt) {
+      if (kt + 1 < KT) fetch(kt + 1);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int ra = wm * 32 + fr, rb = BM + wn * 32 + fr;
+        const f32x4 a = __builtin_bit_cast(f32x4, ring[kt & 1][ra * 8 + swzb(ra, 2 * ks + fh)]);
+        const f32x4 b = __builtin_bit_cast(f32x4, ring[kt & 1][rb * 8 + swzb(rb, 2 * ks + fh)]);
+        // component c of the two halves' pieces: k = 8 ks + 4 fh + c
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[c], b[c], acc, 0, 0, 0);
+      }
+      if (kt + 1 < KT) put((kt + 1) & 1);
+      __syncthreads();
+    }
+  }
+  float *stage = reinterpret_cast<float *>(&ring[0][0]);
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    stage[(wm * 32 + 8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * 32 + fr] = acc[e];
+  __syncthreads();
+  finish_rows<4, 4, BNF, SP, 2>([&](int w) { return stage + w * 32 * SP; }, 0, 1, m0, n0, s_ad,
+                                s_hom, W == nullptr, F, v, T, N, r, y);
+}
+
+// ---------------------------------------------------------------------------
+// bf16: tiles of BM x BN on 4 waves (WM x WN), operands by LDS-direct loads
+// through a ring of NS slots of one 64-deep K step each, one barrier a step.  The ring's slots are separate LDS arrays, so that the
+// compiler does not wait for a load into one slot before it reads another.
+// Pieces past K come from a zero in memory (the last steps only); rows past T
+// and columns past N repeat the last one and are not stored.
+// ---------------------------------------------------------------------------
+__device__ u32x4 g_zero;
+
+template <int OS, int BM, int BNT, int WM, int WN, int NS>
+__global__ __launch_bounds__(256) void expand_ring_kernel(
+    const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
+    const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
+    int n, char *__restrict__ y, int MT, int NT, int rot) {
+  constexpr int MI = BM / WM / 32, NB = BNT / WN / 32;
+  constexpr int IL = (BM + BNT) / 32;  // loads per wave and step
+  constexpr int SLOT = (BM + BNT) * 8, SP = BNT + 4;
+  static_assert(WM * WN == 4 && MI >= 1 && NB >= 1, "four waves of 32 x 32 blocks");
+  static_assert(32 * SP * 4 <= SLOT * 16 && WM <= 2, "a staged row block must fit a slot");
+  static_assert(NS == 3 || NS == 4, "ring of three or four slots");
+  __shared__ u32x4 s0[SLOT], s1[SLOT], s2[SLOT], s3[NS == 4 ? SLOT : 1];
+  __shared__ int s_ad[BM];
+  __shared__ int s_hom[BM / 32];
+  const TileAt at = tile_at(blockIdx.x, MT, NT);
+  if (at.mt < 0) return;
+  const int m0 = at.mt * BM, n0 = at.nt * BNT;
+  const int tid = threadIdx.x, lane = lane_id(),
+            wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wv / WN, wn = wv % WN, fr = lane & 31, fh = lane >> 5;
 
   if (tid < BM) {
@@ -182,121 +394,182 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
 
   if (W) {
-    const int KP = K * ES / 16, KT = (KP + 7) / 8;
-    const u32x4 *src[NLD];
+    const int KP = K / 8, KT = (KP + 7) / 8, KF = KP / 8;  // steps, whole steps
+    const int k_first = rot && KT == KF ? (int)(at.nt * 5u % (unsigned)KT) : 0;
+    const u32x4 *src[IL];
+    int pc[IL];
+    const int dma = wv * (SLOT / 4);
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-      const int row = (tid + 256 * i) >> 3;
-      src[i] = row < BM
-                   ? reinterpret_cast<const u32x4 *>(x + (size_t)min(m0 + row, T - 1) * K * ES)
-                   : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * ES);
+    for (int i = 0; i < IL; ++i) {
+      const int sl = dma + i * 64 + lane, row = sl / 8;
+      pc[i] = swzb(row, sl % 8);
+      src[i] = (row < BM
+                    ? reinterpret_cast<const u32x4 *>(x + (size_t)min(m0 + row, T - 1) * K * 2)
+                    : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * 2)) +
+               pc[i];
     }
-    u32x4 reg[NLD];
-    auto fetch = [&](int kt) {
+    const u32x4 *const zero = &g_zero;
+    // the lane's fragment pieces of its first row blocks (32 rows are 256
+    // pieces further on, under the same swizzle)
+    int ra[4], rb[4];
 #pragma unroll
-      for (int i = 0; i < NLD; ++i) {
-        const int p = kt * 8 + (tid & 7);
-        reg[i] = p < KP ? src[i][p] : u32x4{};
-      }
-    };
-    auto put = [&](int b) {
-      u32x4 *l = reinterpret_cast<u32x4 *>(smem) + b * (BM + BN) * 8;
-#pragma unroll
-      for (int i = 0; i < NLD; ++i) {
-        const int row = (tid + 256 * i) >> 3;
-        l[row * 8 + swz(row, tid & 7)] = reg[i];
-      }
-    };
-    fetch(0);
-    put(0);
-    __syncthreads();
-    for (int kt = 0; kt < KT; ++kt) {
-      if (kt + 1 < KT) fetch(kt + 1);
-      const u32x4 *l = reinterpret_cast<const u32x4 *>(smem) + (kt & 1) * (BM + BN) * 8;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        u32x4 a[MI], b[NB];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const int row = wm * (MI * 32) + i * 32 + fr;
-          a[i] = l[row * 8 + swz(row, 2 * ks + fh)];
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int row = BM + wn * (NB * 32) + j * 32 + fr;
-          b[j] = l[row * 8 + swz(row, 2 * ks + fh)];
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            if constexpr (ES == 2) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0,
-                  0, 0);
-            } else {
-              // component c of the two halves' pieces: k = 8 ks + 4 fh + c
-              const f32x4 fa = __builtin_bit_cast(f32x4, a[i]), fb = __builtin_bit_cast(f32x4, b[j]);
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[c], fb[c], acc[i][j], 0, 0, 0);
-            }
-          }
-      }
-      if (kt + 1 < KT) put((kt + 1) & 1);
-      __syncthreads();
+    for (int ks = 0; ks < 4; ++ks) {
+      ra[ks] = (wm * (MI * 32) + fr) * 8 + swzb(fr, 2 * ks + fh);
+      rb[ks] = (BM + wn * (NB * 32) + fr) * 8 + swzb(fr, 2 * ks + fh);
     }
-  } else {
-    __syncthreads();  // s_ad
+#define MOE_ISSUE(slot, kl, TAIL)                                                            \
+  _Pragma("unroll") for (int i = 0; i < IL; ++i) {                                         \
+    const int kr = (kl) + k_first, ku = kr >= KT ? kr - KT : kr;                           \
+    const u32x4 *g = src[i] + ku * 8;                                                      \
+    if (TAIL && (kl) * 8 + pc[i] >= KP) g = zero;                                          \
+    __builtin_amdgcn_global_load_lds((const void *)g, (lds_void *)((slot) + dma + i * 64), 16, 0, 0); \
   }
+#define MOE_READ(f, slot, ks)                                                                \
+  _Pragma("unroll") for (int i = 0; i < MI; ++i)                                           \
+    f.a[i] = __builtin_bit_cast(bf16x8, (slot)[ra[ks] + i * 256]);                         \
+  _Pragma("unroll") for (int j = 0; j < NB; ++j)                                           \
+    f.b[j] = __builtin_bit_cast(bf16x8, (slot)[rb[ks] + j * 256]);
+#define MOE_MMA(f)                             \
+  mfma_frag<MI, NB>(acc, f, MI);               \
+  interleave_mfma_ds_read<MI * NB, MI + NB>();
+// Step kt, whose first fragments are in f0: each 16-deep part is multiplied
+// while the next one's fragments are read.  Before the last part, every wave
+// has read its slot out and the next step's loads have landed; the barrier
+// makes both known, the slot takes step kt + NS, and the next step's first
+// fragments are read under the last multiplies.
+#define MOE_STEP(cur, nxt, kt, TAIL)                                       \
+  MOE_READ(f1, cur, 1)                                                     \
+  MOE_MMA(f0)                                                              \
+  MOE_READ(f0, cur, 2)                                                     \
+  MOE_MMA(f1)                                                              \
+  MOE_READ(f1, cur, 3)                                                     \
+  MOE_MMA(f0)                                                              \
+  wait_vmcnt_lgkm0<(NS - 2) * IL>();                                       \
+  stage_barrier();                                                         \
+  MOE_ISSUE(cur, (kt) + NS, TAIL)                                          \
+  MOE_READ(f0, nxt, 0)                                                     \
+  MOE_MMA(f1)
+#define MOE_PERIOD(kt, TAIL)             \
+  MOE_STEP(s0, s1, kt, TAIL)             \
+  MOE_STEP(s1, s2, (kt) + 1, TAIL)       \
+  if constexpr (NS == 4) {               \
+    MOE_STEP(s2, s3, (kt) + 2, TAIL)     \
+    MOE_STEP(s3, s0, (kt) + 3, TAIL)     \
+  } else {                               \
+    MOE_STEP(s2, s0, (kt) + 2, TAIL)     \
+  }
+    MOE_ISSUE(s0, 0, true)
+    MOE_ISSUE(s1, 1, true)
+    MOE_ISSUE(s2, 2, true)
+    if constexpr (NS == 4) {
+      MOE_ISSUE(s3, 3, true)
+    }
+    wait_vmcnt<(NS - 1) * IL>();
+    stage_barrier();
+    Frag<MI, NB> f0, f1;
+    MOE_READ(f0, s0, 0)
+    int kt = 0;
+    // a period loads up to step kt + 2 NS - 1; the steps past the last one
+    // multiply zeros
+    for (; kt + 2 * NS <= KF; kt += NS) {
+      MOE_PERIOD(kt, false)
+    }
+    for (; kt < KT; kt += NS) {
+      MOE_PERIOD(kt, true)
+    }
+    wait_vmcnt<0>();  // no LDS-direct load may still be landing
+#undef MOE_PERIOD
+#undef MOE_STEP
+#undef MOE_MMA
+#undef MOE_READ
+#undef MOE_ISSUE
+  }
+  __syncthreads();  // s_ad; every wave is done with the ring
 
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_ad, s_hom, wm * MI, lane == 0 && wn == 0, m0,
+                                           n0 + wn * (NB * 32), F, v, T, N, r, fr, fh);
+  // 32 rows of every wave row at a time meet in LDS in fp32
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int row = wm * (MI * 32) + i * 32 + fr;
-    const int a = s_ad[row], a0 = __builtin_amdgcn_readfirstlane(a);
-    const bool hom = ES == 2 && a0 >= 0 && __all(a == a0);
-    if (lane == 0 && wn == 0) s_hom[wm * MI + i] = hom;
-    if constexpr (ES == 2) {
-      if (hom) {
-        int nn[NB];
-#pragma unroll
-        for (int j = 0; j < NB; ++j) nn[j] = min(n0 + wn * (NB * 32) + j * 32 + fr, N - 1);
-        mma_low_rank<OS == 2 ? 2 : 3, NB>(acc[i], v, F + (size_t)a0 * r * N * ES, r, N,
-                                          (size_t)min(m0 + row, T - 1), nn, fh);
-      }
-    }
-  }
-  // the tile meets in LDS in fp32 (the ring is free after the last barrier),
-  // then every thread finishes whole 8-column pieces of rows
-  float *stage = reinterpret_cast<float *>(smem);
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
+    float *mine = reinterpret_cast<float *>(wm == 0 ? s0 : s1);
+    if (i > 0) __syncthreads();
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        stage[(wm * (MI * 32) + i * 32 + 8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * (NB * 32) +
-              j * 32 + fr] = acc[i][j][e];
+        mine[(8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * (NB * 32) + j * 32 + fr] = acc[i][j][e];
+    __syncthreads();
+    finish_rows<2, OS, BNT, SP, WM>(
+        [&](int w) { return reinterpret_cast<const float *>(w == 0 ? s0 : s1); }, i, MI, m0, n0,
+        s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16, large batches: 256 x 256 tiles on the grouped GEMM's K loop (four
+// waves of 128 x 128, which reads half as many operand bytes from LDS per
+// multiply as 64 x 64).  K % 128 == 0.
+// ---------------------------------------------------------------------------
+template <int OS>
+__global__ __launch_bounds__(256, 1) void expand_big_kernel(
+    const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
+    const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
+    int n, char *__restrict__ y, int MT, int NT) {
+  constexpr int NW = 4, NWN = 2, MI = 4, NB = 4;
+  constexpr int SLOTS_A2 = BM_MAX * PIECES_B;
+  constexpr int IA = SLOTS_A2 / NW / 64, IB = SLOTS_B2 / NW / 64;
+  __shared__ u32x4 sA0[SLOTS_A2MAX], sA1[SLOTS_A2MAX];
+  __shared__ u32x4 sB0[SLOTS_B2], sB1[SLOTS_B2], sB2[SLOTS_B2];
+  const TileAt at = tile_at(blockIdx.x, MT, NT);
+  if (at.mt < 0) return;
+  const int m0 = at.mt * BM_MAX, n0 = at.nt * BN;
+  const int tid = threadIdx.x, lane = lane_id(),
+            wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wv / NWN, wn = wv % NWN, fr = lane & 31, fh = lane >> 5;
+  const uint16_t *ga[IA], *gb[IB];
+  const int dma_a = wv * (SLOTS_A2 / NW), dma_b = wv * (SLOTS_B2 / NW);
+#pragma unroll
+  for (int i = 0; i < IA; ++i) {
+    const int sl = dma_a + i * 64 + lane, row = sl / PIECES_B;
+    ga[i] = reinterpret_cast<const uint16_t *>(x) + (size_t)min(m0 + row, T - 1) * K +
+            swzb(row, sl % PIECES_B) * 8;
+  }
+#pragma unroll
+  for (int i = 0; i < IB; ++i) {
+    const int sl = dma_b + i * 64 + lane, row = sl / PIECES_B;
+    gb[i] = reinterpret_cast<const uint16_t *>(W) + (size_t)min(n0 + row, N - 1) * ldw +
+            swzb(row, sl % PIECES_B) * 8;
+  }
+  f32x16 acc[MI][NB];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
+  tile_k_loop<false, MI, NB, NWN, IA, IB>(acc, ga, gb, K / BK, dma_a, dma_b, wm, wn, fr, fh, MI, sA0,
+                                          sA1, sB0, sB1, sB2);
+  __syncthreads();  // every wave is done with the rings
+  int *const s_ad = reinterpret_cast<int *>(sA0), *const s_hom = s_ad + BM_MAX;
+  {
+    const int a = adapter[min(m0 + tid, T - 1)];
+    s_ad[tid] = a >= 0 && a < n ? a : -1;
+  }
   __syncthreads();
-  const bool vec = N % 8 == 0;  // rows of F and of y are then 16-byte aligned
-  constexpr int CG = BN / 8;
-  for (int q = tid; q < BM * CG; q += 256) {
-    const int row = q / CG, c = (q % CG) * 8, t = m0 + row, col = n0 + c;
-    if (t >= T || col >= N) continue;
-    const int have = N - col;
-    float f[8];
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_ad, s_hom, wm * MI, lane == 0 && wn == 0, m0,
+                                           n0 + wn * (NB * 32), F, v, T, N, r, fr, fh);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = stage[row * SP + c + i];
-    const int a = s_ad[row];
-    if (a >= 0 && !s_hom[row / 32])
-      add_low_rank<ES>(f, v + (size_t)t * r, F + (size_t)a * r * N * ES, r, N, col, vec, have);
-    if (!W) {
-      float old[8];
-      ld8<OS>(y, (size_t)t * N + col, vec, have, old);
+  for (int i = 0; i < MI; ++i) {
+    // 32 rows of both wave rows: 32 x 256 fp32 are one B slot
+    float *mine = reinterpret_cast<float *>(wm == 0 ? sB0 : sB1);
+    if (i > 0) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] += old[i];
-    }
-    st8<OS>(y, (size_t)t * N + col, vec, have, f);
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        mine[(8 * (e >> 2) + 4 * fh + (e & 3)) * BN + wn * (NB * 32) + j * 32 + fr] = acc[i][j][e];
+    __syncthreads();
+    finish_rows<2, OS, BN, BN, 2>(
+        [&](int w) { return reinterpret_cast<const float *>(w == 0 ? sB0 : sB1); }, i, MI, m0, n0,
+        s_ad, s_hom, false, F, v, T, N, r, y);
   }
 }
 
@@ -326,17 +599,11 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b] = f32x4{};
   // a wave takes two neighbouring groups of 4 pieces (whole 128-byte lines)
-  // out of each 16
+  // out of each 16; the last, partial chunk reads zeros behind K
   constexpr int U = MB <= 2 ? 8 : 4;
-  for (int g0 = 2 * wv; g0 * 4 < KP; g0 += U * kRowWaves) {
-    u32x4 wa[U], xa[U][MB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = (g0 + (u & 1) + (u >> 1) * 2 * kRowWaves) * 4 + fq;
-      wa[u] = p < KP ? wp[p] : u32x4{};
-#pragma unroll
-      for (int b = 0; b < MB; ++b) xa[u][b] = p < KP ? xp[b][p] : u32x4{};
-    }
+  constexpr int CHUNK = U * kRowWaves * 4;  // pieces that the workgroup takes at once
+  auto multiply = [&](const u32x4 (&wa)[U], const u32x4 (&xa)[U][MB]) {
+    __builtin_amdgcn_sched_barrier(0);  // every load of the chunk is issued first
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -344,6 +611,29 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
         acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa[u][b]),
                                                          __builtin_bit_cast(bf16x8, wa[u]), acc[b],
                                                          0, 0, 0);
+  };
+  int p0 = 0;
+  for (; p0 + CHUNK <= KP; p0 += CHUNK) {
+    u32x4 wa[U], xa[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + (2 * wv + (u & 1) + (u >> 1) * 2 * kRowWaves) * 4 + fq;
+      wa[u] = wp[p];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) xa[u][b] = xp[b][p];
+    }
+    multiply(wa, xa);
+  }
+  if (p0 < KP) {
+    u32x4 wa[U], xa[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + (2 * wv + (u & 1) + (u >> 1) * 2 * kRowWaves) * 4 + fq;
+      wa[u] = load_piece(wp, p, KP);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) xa[u][b] = load_piece(xp[b], p, KP);
+    }
+    multiply(wa, xa);
   }
 #pragma unroll
   for (int b = 0; b < MB; ++b)
@@ -375,62 +665,70 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
 // rows up to which expand_rows_kernel runs (bf16 with a W)
 constexpr int kExpandRowsMax = 64;
 
+// Tile shapes of the bf16 kernels, and what a 64-deep K step and the rest of a
+// tile take on a CU, in ns: measured with one tile per CU on 96 to 4096 rows,
+// K from 2048 to 7168.
 struct Shape {
-  int BM, BN;
+  int BM, BN, step, fixed;
 };
+constexpr Shape kShapes[] = {
+    {256, 256, 1750, 12000}, {128, 128, 700, 5000}, {64, 128, 480, 4000}, {64, 64, 310, 3000}};
+constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 
-// The tile shape whose rounds over the CUs cost least: a K step of 128 bytes
-// takes the larger of its matrix-core time and its L2 time.
-Shape pick_tile(int T, int N, int cus, bool f32) {
-  const Shape all[] = {{128, 128}, {128, 64}, {64, 64}, {32, 128}};
-  Shape best = all[0];
+// the shape whose rounds over the CUs cost least
+int pick_tile(int T, int N, int K, bool with_w, int cus) {
+  int best = 1;
   double least = 1e300;
-  for (const Shape &s : all) {
+  for (int i = K % 128 == 0 && with_w ? 0 : 1; i < kNumShapes; ++i) {
+    const Shape &s = kShapes[i];
     const double tiles = (double)((T + s.BM - 1) / s.BM) * ((N + s.BN - 1) / s.BN);
-    const double rounds = tiles <= cus ? 1.0 : tiles / cus > 4 ? tiles / cus : (double)((long long)(tiles + cus - 1) / cus);
-    const double mma = s.BM * s.BN / (f32 ? 4.0 : 20.0), l2 = (s.BM + s.BN) * 2.7;
-    const double cost = rounds * (mma > l2 ? mma : l2);
+    double rounds = tiles / (cus > 0 ? cus : 256);
+    if (rounds < 8) rounds = (double)(long long)(rounds + 0.9999);
+    const double cost = rounds * ((K + 63) / 64 * (double)s.step + s.fixed);
     if (cost < least) {
       least = cost;
-      best = s;
+      best = i;
     }
   }
   return best;
 }
 
-template <int ES, int OS, int BM, int BN, int WM, int WN>
-void launch_tile(const char *x, const char *W, int ldw, const char *F, const float *v,
-                 const int32_t *adapter, int T, int N, int K, int r, int n, char *y, hipStream_t s) {
-  const int MT = (T + BM - 1) / BM, NT = (N + BN - 1) / BN;
-  hipLaunchKernelGGL((expand_tile_kernel<ES, OS, BM, BN, WM, WN>), dim3(tile_grid(MT, NT)), dim3(256),
-                     0, s, x, W, ldw, F, v, adapter, T, N, K, r, n, y, MT, NT);
+template <class Kernel, class... More>
+void launch_tiles(Kernel kernel, int BM, int BNT, const char *x, const char *W, int ldw,
+                  const char *F, const float *v, const int32_t *adapter, int T, int N, int K, int r,
+                  int n, char *y, hipStream_t s, More... more) {
+  const int MT = (T + BM - 1) / BM, NT = (N + BNT - 1) / BNT;
+  hipLaunchKernelGGL(kernel, dim3(tile_grid(MT, NT)), dim3(256), 0, s, x, W, ldw, F, v, adapter, T,
+                     N, K, r, n, y, MT, NT, more...);
 }
 
-template <int ES, int OS>
-void launch_t(const char *x, const char *W, int ldw, const char *F, const float *v,
-              const int32_t *adapter, int T, int N, int K, int r, int n, char *y, int cus,
-              hipStream_t s) {
-  if constexpr (ES == 2) {
-    if (W && T <= kExpandRowsMax) {
-      const dim3 grid((N + 15) / 16), block(kRowWaves * kWave);
+template <int OS>
+void launch_bf16(const char *x, const char *W, int ldw, const char *F, const float *v,
+                 const int32_t *adapter, int T, int N, int K, int r, int n, char *y, int cus,
+                 hipStream_t s) {
+  if (W && T <= kExpandRowsMax) {
+    const dim3 grid((N + 15) / 16), block(kRowWaves * kWave);
 #define MOE_ROWS(MB)                                                                             \
   hipLaunchKernelGGL((expand_rows_kernel<OS, MB>), grid, block, 0, s, x, W, ldw, F, v, adapter, T, \
                      N, K, r, n, y)
-      if (T <= 16) MOE_ROWS(1);
-      else if (T <= 32) MOE_ROWS(2);
-      else MOE_ROWS(4);
+    if (T <= 16) MOE_ROWS(1);
+    else if (T <= 32) MOE_ROWS(2);
+    else MOE_ROWS(4);
 #undef MOE_ROWS
-      return;
-    }
+    return;
   }
-  const Shape p = pick_tile(T, N, cus, ES == 4);
-#define MOE_TILE(BM, BN, WM, WN) \
-  launch_tile<ES, OS, BM, BN, WM, WN>(x, W, ldw, F, v, adapter, T, N, K, r, n, y, s)
-  if (p.BM == 128 && p.BN == 128) MOE_TILE(128, 128, 2, 2);
-  else if (p.BM == 128) MOE_TILE(128, 64, 2, 2);
-  else if (p.BM == 64) MOE_TILE(64, 64, 2, 2);
-  else MOE_TILE(32, 128, 1, 4);
-#undef MOE_TILE
+  const int rot = T <= 128;
+#define MOE_TILES(kernel, BM, BNT) \
+  launch_tiles(kernel, BM, BNT, x, W, ldw, F, v, adapter, T, N, K, r, n, y, s, rot)
+  switch (pick_tile(T, N, K, W != nullptr, cus)) {
+    case 0:
+      launch_tiles(expand_big_kernel<OS>, 256, 256, x, W, ldw, F, v, adapter, T, N, K, r, n, y, s);
+      break;
+    case 1: MOE_TILES((expand_ring_kernel<OS, 128, 128, 2, 2, 4>), 128, 128); break;
+    case 2: MOE_TILES((expand_ring_kernel<OS, 64, 128, 1, 4, 4>), 64, 128); break;
+    default: MOE_TILES((expand_ring_kernel<OS, 64, 64, 2, 2, 4>), 64, 64); break;
+  }
+#undef MOE_TILES
 }
 
 }  // namespace
@@ -441,8 +739,11 @@ hipError_t launch_lora_expand(const void *x, const void *W, int ldw, const void 
   const char *xb = static_cast<const char *>(x), *wb = static_cast<const char *>(W),
              *fb = static_cast<const char *>(F);
   char *yb = static_cast<char *>(y);
-  if (dt == MOE_F32) launch_t<4, 4>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
-  else if (y_dt == MOE_F32) launch_t<2, 4>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
-  else launch_t<2, 2>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
+  if (dt == MOE_F32)
+    launch_tiles(expand_f32_kernel, 64, 64, xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, s);
+  else if (y_dt == MOE_F32)
+    launch_bf16<4>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
+  else
+    launch_bf16<2>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
   return hipGetLastError();
 }

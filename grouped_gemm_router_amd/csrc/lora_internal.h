@@ -10,6 +10,17 @@ namespace moe {
 // rows up to which the shrink runs one wave per (row, rank)
 constexpr int kShrinkRowMax = 128;
 
+// Piece p of a row of np pieces, zero behind the row's end.  The load itself is
+// unconditional: under a condition, each load of a batch gets its own branch
+// and wait.
+__device__ __forceinline__ u32x4 load_piece(const u32x4 *row, int p, int np) {
+  const u32x4 q = row[min(p, np - 1)];
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = p < np ? q[i] : 0u;
+  return r;
+}
+
 // fp32 -> the bf16 terms of a sum that holds it: f = t[0] + t[1] (+ t[2]),
 // each the rounded rest of the one before.  Two terms keep 16 bits of f,
 // three all 24.

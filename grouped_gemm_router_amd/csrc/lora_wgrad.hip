@@ -12,8 +12,7 @@
 // is what bounds this (2 r flops per 2 bytes).  u and v are fp32 and enter as
 // three bf16 terms each, so no bit of them is lost.  A unit that is all of
 // its adapter writes the gradient itself; the slices of a longer one go to
-// the workspace and the third launch adds them in order (and writes zeros for
-// adapters without rows).
+// the workspace and a third launch adds them in order.
 #include "lora_internal.h"
 
 namespace {
@@ -23,10 +22,12 @@ using namespace moe;
 constexpr int kPlanWaves = 16;
 constexpr int kColTile = 128;
 
-// rows per unit: enough units to fill the chip, at most 64 slices to add
+// rows per unit: at most 64 slices to add; batches of up to kUnitRows rows
+// are never sliced and need no third launch
+constexpr int kUnitRows = 1024;
 int unit_rows(int T) {
   const int by = ((T + 31) / 32 + 31) / 32 * 32;
-  return by > 256 ? by : 256;
+  return by > kUnitRows ? by : kUnitRows;
 }
 
 struct Unit {
@@ -41,7 +42,7 @@ struct Ws {
 Ws layout(int T, int N, int K, int r, int n) {
   Ws w;
   w.TS = unit_rows(T);
-  w.max_units = T / w.TS + (n < T ? n : T);
+  w.max_units = T / w.TS + n;  // (an adapter without rows has one of no rows)
   // an adapter of c > TS rows has fewer than 2 c / TS units
   const size_t slots = T <= w.TS ? 0 : 2 * (size_t)T / w.TS + 1;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(kPlanWaves *kWave) void wgrad_plan_kernel(
   int mine = 0;
   if (tid < n)
     for (int w = 0; w < kPlanWaves; ++w) mine += count[w][tid];
-  const int nu = (mine + TS - 1) / TS;
+  const int nu = tid < n ? max(1, (mine + TS - 1) / TS) : 0;
   int rows_all, units_all, slots_all;
   const int pos = block_scan(mine, s_w, &rows_all);
   const int u0 = block_scan(nu, s_w, &units_all);
@@ -148,8 +149,7 @@ __global__ __launch_bounds__(256) void wgrad_kernel(
   const float *p = is_a ? u : v;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int fr = lane & 15, fq = lane >> 4;
-  const int col = c0 + 8 * fr;
-  const bool in_c = col < C;  // C is a multiple of 8
+  const int col = min(c0 + 8 * fr, C - 8);  // C is a multiple of 8
   f32x4 acc[NR][8];
 #pragma unroll
   for (int b = 0; b < NR; ++b)
@@ -157,28 +157,32 @@ __global__ __launch_bounds__(256) void wgrad_kernel(
     for (int f = 0; f < 8; ++f) acc[b][f] = f32x4{};
 
   for (int s = wv * 32; s < un.count; s += 4 * 32) {
-    // rows past the unit's end read as zero in both operands
-    int id[8];
+    // rows past the unit's end load the last one and count as zero in both
+    // operands (no load is under a condition: the loads are in flight
+    // together); columns past C and ranks past r load the last ones and are
+    // not stored
+    size_t t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = s + fq * 8 + i;
-      id[i] = k < un.count ? order[un.pos + k] : -1;
-    }
+    for (int i = 0; i < 8; ++i) t[i] = order[un.pos + min(s + fq * 8 + i, un.count - 1)];
     u32x4 qv[8][ES / 2];
     float pv[NR][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool in = id[i] >= 0;
-      const size_t t = in ? id[i] : 0;
 #pragma unroll
       for (int h = 0; h < ES / 2; ++h)
-        qv[i][h] = in && in_c ? *reinterpret_cast<const u32x4 *>(q + (t * C + col) * ES + 16 * h)
-                              : u32x4{};
+        qv[i][h] = *reinterpret_cast<const u32x4 *>(q + (t[i] * C + col) * ES + 16 * h);
 #pragma unroll
-      for (int b = 0; b < NR; ++b) {
-        const int j = j0 + b * 16 + fr;
-        pv[b][i] = in && j < r ? p[t * r + j] : 0.f;
-      }
+      for (int b = 0; b < NR; ++b) pv[b][i] = p[t[i] * r + min(j0 + b * 16 + fr, r - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = s + fq * 8 + i < un.count;
+#pragma unroll
+      for (int h = 0; h < ES / 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) qv[i][h][c] = in ? qv[i][h][c] : 0u;
+#pragma unroll
+      for (int b = 0; b < NR; ++b) pv[b][i] = in ? pv[b][i] : 0.f;
     }
     if constexpr (ES == 2) {
       bf16x8 pt[NR][3];
@@ -240,7 +244,7 @@ __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const int2 *__restric
                                                            float *__restrict__ dB) {
   const int a = blockIdx.y;
   const int2 s = adapters[a];
-  if (s.y == 1) return;
+  if (s.y <= 1) return;
   const int wide = (K + N) / 4;
   const long long q = (long long)blockIdx.x * 256 + threadIdx.x;
   if (q >= (long long)r * wide) return;
@@ -283,10 +287,9 @@ hipError_t launch_lora_wgrad(const void *dy, const void *x, int dt, const float 
                      reinterpret_cast<int32_t *>(b + w.order), reinterpret_cast<Unit *>(b + w.units),
                      reinterpret_cast<int2 *>(b + w.adapters),
                      reinterpret_cast<int32_t *>(b + w.n_units));
-  if (T > 0) {
-    if (dt == MOE_BF16) launch_t<2>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
-    else launch_t<4>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
-  }
+  if (dt == MOE_BF16) launch_t<2>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
+  else launch_t<4>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
+  if (T <= w.TS) return hipGetLastError();
   const long long pieces = (long long)r * ((K + N) / 4);
   hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)((pieces + 255) / 256), n), dim3(256), 0, s,
                      reinterpret_cast<const int2 *>(b + w.adapters),
