@@ -6,10 +6,11 @@
 // in both directions (T E values of exp against T E 4 bytes of traffic for
 // storing it).
 //
-// A wave takes 64 / L tokens at once, L lanes each; a lane holds 4 NP
-// consecutive-by-four experts (16-byte loads; E % 4 == 0) or NP strided ones.
+// A wave takes 64 / L tokens at once, L lanes each; a lane holds NP groups of
+// four neighbouring experts (16-byte loads; E % 4 == 0) or NP single ones.
 // Everything is one pass over the logits: HBM-bound on large batches,
-// latency-bound on small ones.
+// latency-bound on small ones, so a batch of loads is always in flight before
+// the one before it is used, and the sums over a token's lanes are DPP.
 #include "moe_internal.h"
 #include "../../include/moe_balance.h"
 
@@ -20,62 +21,72 @@ using namespace moe;
 constexpr int kWavesP = 8;              // waves per workgroup
 constexpr int kThreadsP = kWavesP * kWave;
 
-// e^x for x <= 0: exp2 of the rounded product x log2(e), corrected to first
-// order by the product's rounding error and the low part of log2(e).  The
-// hardware exp2 is within 1 ulp; without the correction the error grows to
-// |x| ulp.
+// e^x for x <= 0 by the hardware exp2 (within 1 ulp) of the rounded product
+// x log2(e): |x| 2^-24 more, so that the large probabilities, whose x is
+// small, keep all their bits.  -inf gives 0.
 __device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f, kLn2 = 0.693147182f;
-  const float t = x * kHi;
-  if (!(t > -150.f)) return x != x ? x : 0.f;  // underflows (also x = -inf)
-  const float lo = fmaf(x, kHi, -t) + x * kLo;
-  const float r = __builtin_amdgcn_exp2f(t);
-  return fmaf(r, lo * kLn2, r);
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
 }
 
-// Token t's sequence: the first s with off[s + 1] > t, S if there is none
-// (offsets as stored; whatever they hold, the result is in [0, S]).
+// The first sequence s with off[s + 1] > t, S if there is none: 64 probes at a
+// time by the lanes of a wave (one round of loads for up to 64 sequences,
+// three for any number).  Whatever the offsets hold, the result is in [0, S].
+// Must be called by a whole wave.
 __device__ __forceinline__ int sequence_of(const int32_t *off, int S, int t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid + 1] > t) hi = mid; else lo = mid + 1;
+  int lo = 0, n = S;  // sequences before lo end at t or before, those from lo + n on do not
+  while (n > 0) {
+    const int step = (n + kWave - 1) / kWave;
+    const int i = lo + min(((int)lane_id() + 1) * step, n) - 1;
+    const unsigned long long behind = __ballot(off[i + 1] > t);
+    if (behind == 0) return lo + n;
+    const int f = __builtin_ctzll(behind), hit = lo + min((f + 1) * step, n) - 1;
+    lo += f * step;
+    n = hit - lo;
   }
   return lo;
 }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// The lanes' share of one row of E values.
-template <int NP, bool VEC>
+// The lanes' share of one row of E values: a token has L lanes (a power of
+// two); lane l's values are those of experts expert(i, l).
+template <int L_, int NP, bool VEC>
 struct Row {
-  static constexpr int V = VEC ? 4 * NP : NP;
+  static constexpr int L = L_, V = VEC ? 4 * NP : NP;
   float v[V];
-  static __device__ __forceinline__ int expert(int i, int l, int L) {
+  static __device__ __forceinline__ int expert(int i, int l) {
     return VEC ? ((i >> 2) * L + l) * 4 + (i & 3) : i * L + l;
   }
-  __device__ __forceinline__ void load(const float *row, int l, int L, int E) {
+  // -inf behind E
+  __device__ __forceinline__ void load(const float *row, int l, int E) {
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int e = (i * L + l) * 4;
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (e < E) q = *reinterpret_cast<const float4 *>(row + e);
-        v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+        const f32x4 q = *reinterpret_cast<const f32x4 *>(row + min(e, E - 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[4 * i + c] = q[c];
+      }
+      if (E < L * V) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = expert(i, l) < E ? v[i] : -INFINITY;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) v[i] = i * L + l < E ? row[i * L + l] : -INFINITY;
+      for (int i = 0; i < NP; ++i) {
+        const float q = row[min(i * L + l, E - 1)];
+        v[i] = i * L + l < E ? q : -INFINITY;
+      }
     }
   }
-  __device__ __forceinline__ void store(float *row, int l, int L, int E) const {
+  __device__ __forceinline__ void store(float *row, int l, int E) const {
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int e = (i * L + l) * 4;
         if (e < E)
-          *reinterpret_cast<float4 *>(row + e) =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          *reinterpret_cast<f32x4 *>(row + e) =
+              f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
       }
     } else {
 #pragma unroll
@@ -83,120 +94,208 @@ struct Row {
         if (i * L + l < E) row[i * L + l] = v[i];
     }
   }
+  __device__ __forceinline__ void fill(float f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = f;
+  }
 };
 
-// sum / maximum over the L lanes of a token (L a power of two)
-__device__ __forceinline__ float lanes_sum(float v, int L) {
-  for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+// f over the L lanes of a token, the same value in each of them: exchanges
+// inside a row of 16 lanes by DPP (neighbours, pairs, mirrored halves), then
+// the swaps of 16- and 32-lane halves.  The order is fixed.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(dpp<CTRL>(__float_as_int(v)));
+}
+template <int L, class T, class F>
+__device__ __forceinline__ T over_lanes(T v, F f) {
+  if constexpr (L >= 2) v = f(v, dpp<0xB1>(v));    // lane ^ 1
+  if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));    // lane ^ 2
+  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));   // 7 - lane of 8
+  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));  // 15 - lane of 16
+  if constexpr (L >= 32) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto q = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const unsigned a = q[0], b = q[1];
+    v = f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+  }
+  if constexpr (L >= 64) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned a = q[0], b = q[1];
+    v = f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+  }
   return v;
 }
-__device__ __forceinline__ float lanes_max(float v, int L) {
-  for (int o = L >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return over_lanes<L>(v, [](float a, float b) { return a + b; });
+}
+// the maximum by the bits as integers of the same order: one instruction an
+// exchange, where a floating maximum first quiets both operands
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  int u = __float_as_int(v);
+  u ^= (u >> 31) & 0x7fffffff;
+  u = over_lanes<L>(u, [](int a, int b) { return max(a, b); });
+  u ^= (u >> 31) & 0x7fffffff;
+  return __int_as_float(u);
 }
 
 // logits -> probabilities in place; a row of -inf only becomes zeros
-template <int NP, bool VEC>
-__device__ __forceinline__ void softmax_row(Row<NP, VEC> &x, int L) {
-  constexpr int V = Row<NP, VEC>::V;
+template <class R>
+__device__ __forceinline__ void softmax_row(R &x) {
   float m = x.v[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, x.v[i]);
-  m = lanes_max(m, L);
+  for (int i = 1; i < R::V; ++i) m = fmaxf(m, x.v[i]);
+  m = lanes_max<R::L>(m);
   if (m == -INFINITY) m = 0.f;
   float z = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < R::V; ++i) {
     x.v[i] = exp_neg(x.v[i] - m);
     z += x.v[i];
   }
-  z = lanes_sum(z, L);
-  const float inv = z != 0.f ? 1.f / z : 0.f;
+  z = lanes_sum<R::L>(z);
+  const float inv = z != 0.f ? __builtin_amdgcn_rcpf(z) : 0.f;  // (within 1 ulp)
 #pragma unroll
-  for (int i = 0; i < V; ++i) x.v[i] *= inv;
+  for (int i = 0; i < R::V; ++i) x.v[i] *= inv;
 }
 
 // tokens in flight per token slot: enough loads to cover the latency without
 // running out of registers
-template <int NP, bool VEC>
-constexpr int unroll_of() { return Row<NP, VEC>::V <= 4 ? 4 : (Row<NP, VEC>::V <= 8 ? 2 : 1); }
+template <class R>
+constexpr int unroll_of() { return R::V <= 4 ? 4 : (R::V <= 8 ? 2 : 1); }
 
 // ---------------------------------------------------------------------------
 // loss, first launch: block b (C tokens) writes, for every sequence s that
 // has tokens in it, slot b + s: the sums of the probabilities, the counts
 // and the number of tokens that take part.  b + s is a slot of its own for
 // each such pair: going along the tokens, b or s grows from pair to pair and
-// neither ever falls.
+// neither ever falls.  A batch of one block and one sequence is finished here.
 // ---------------------------------------------------------------------------
-template <int NP, bool VEC>
+struct LossOut {
+  int32_t *counts;
+  float *probs;
+  int32_t *tokens;
+  float *loss;
+};
+
+template <class R>
 __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
     const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
     const int32_t *__restrict__ off, const uint8_t *__restrict__ mask, int T, int E, int k, int S,
-    int C, int L, float *__restrict__ slot_p, int32_t *__restrict__ slot_c,
-    int32_t *__restrict__ slot_n, int32_t *__restrict__ ticket) {
-  using R = Row<NP, VEC>;
-  constexpr int U = unroll_of<NP, VEC>();
+    int C, float alpha, float *__restrict__ slot_p, int32_t *__restrict__ slot_c,
+    int32_t *__restrict__ slot_n, int32_t *__restrict__ ticket, LossOut out) {
+  constexpr int U = unroll_of<R>(), L = R::L, nq = kWave / L;
   __shared__ float s_p[kWavesP][MOE_MAX_EXPERTS];
   __shared__ int s_c[MOE_MAX_EXPERTS];
   __shared__ int s_n;
+  __shared__ float s_w[kWavesP];
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
-  const int l = lane & (L - 1), q = lane / L, nq = kWave / L;
+  const int l = lane & (L - 1), q = lane / L;
   const int b = blockIdx.x, b0 = b * C, b1 = min(T, b0 + C);
+  const bool whole = gridDim.x == 1 && S == 1;
   if (b == 0 && tid == 0) *ticket = 0;
-  int s = off ? sequence_of(off, S, b0) : 0;
+  constexpr int step = kWavesP * nq;  // token slots of the workgroup
+  // A batch is U tokens of every slot.  The first one is loaded before
+  // anything else is looked up: which tokens take part in which sequence is
+  // decided when its probabilities are there.
+  R x[U];
+  bool on[U];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * step, tc = max(min(t, b1 - 1), 0);
+      if (b1 > b0) x[u].load(logits + (size_t)tc * E, l, E);
+      on[u] = t < b1;
+      if (mask) on[u] = on[u] && mask[tc];
+    }
+  };
+  const int slot = b0 + wv * nq + q;  // the lane's first token
+  load(slot);
+  // entry i of the block: an expert, -1 if it counts for none
+  const int entries = (b1 - b0) * k;
+  auto entry = [&](int i) {
+    const int ic = max(min(i, entries - 1), 0);
+    const int e = entries > 0 ? topk_idx[(size_t)b0 * k + ic] : -1;
+    bool in = i < entries && e >= 0 && e < E;
+    if (mask && entries > 0) in = in && mask[b0 + ic / k];
+    return in ? e : -1;
+  };
+  const int e0 = entry(tid);
+  int s = off && !whole ? sequence_of(off, S, b0) : 0;
+  bool first = true;
   for (; s < S; ++s) {
     const int lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
-    if (lo >= b1) break;
+    if (lo >= b1 && !whole) break;
     const int ta = max(lo, b0), tb = min(hi, b1);
-    if (ta >= tb) continue;
+    if (ta >= tb && !whole) continue;
     for (int e = tid; e < E; e += kThreadsP) s_c[e] = 0;
     if (tid == 0) s_n = 0;
     __syncthreads();
-    for (int i = tid; i < (tb - ta) * k; i += kThreadsP) {
-      const int e = topk_idx[(size_t)ta * k + i];
-      if ((!mask || mask[ta + i / k]) && e >= 0 && e < E) atomicAdd(&s_c[e], 1);
+    for (int i = tid; i < entries; i += kThreadsP) {
+      const int e = i == tid ? e0 : entry(i), t = b0 + i / k;
+      if (e >= 0 && t >= ta && t < tb) atomicAdd(&s_c[e], 1);
     }
-    for (int t = ta + tid; t < tb; t += kThreadsP)
-      if (!mask || mask[t]) atomicAdd(&s_n, 1);
+    int n_mine = 0;  // tokens of the wave that take part
     float acc[R::V];
 #pragma unroll
     for (int i = 0; i < R::V; ++i) acc[i] = 0.f;
-    const int step = kWavesP * nq;
-    for (int t0 = ta + wv * nq + q; t0 - q < tb; t0 += U * step) {
-      R x[U];
-      bool on[U];
+    for (int t0 = slot; t0 - q < b1; t0 += U * step) {
+      if (!first) load(t0);
+      first = b1 - b0 <= U * step;  // the block is one batch: it stays loaded
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * step;
-        on[u] = t < tb && (!mask || mask[t]);
-        if (on[u]) {
-          x[u].load(logits + (size_t)t * E, l, L, E);
-        } else {
+        const bool in = on[u] && t >= ta && t < tb;
+        n_mine += __popcll(__ballot(in && l == 0));
+        R p = x[u];
+        softmax_row(p);
 #pragma unroll
-          for (int i = 0; i < R::V; ++i) x[u].v[i] = -INFINITY;  // probability 0
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        softmax_row(x[u], L);
-#pragma unroll
-        for (int i = 0; i < R::V; ++i) acc[i] += x[u].v[i];
+        for (int i = 0; i < R::V; ++i) acc[i] += in ? p.v[i] : 0.f;
       }
     }
 #pragma unroll
     for (int i = 0; i < R::V; ++i) {
       for (int o = L; o < kWave; o <<= 1) acc[i] += __shfl_xor(acc[i], o, kWave);
-      const int e = R::expert(i, l, L);
+      const int e = R::expert(i, l);
       if (q == 0 && e < E) s_p[wv][e] = acc[i];
     }
+    if (lane == 0) atomicAdd(&s_n, n_mine);
     __syncthreads();
     const size_t base = (size_t)(b + s) * E;
+    float dot = 0.f;
+    const float fn = (float)max(s_n, 1);
     for (int e = tid; e < E; e += kThreadsP) {
       float p = s_p[0][e];
 #pragma unroll
       for (int w = 1; w < kWavesP; ++w) p += s_p[w][e];
-      slot_p[base + e] = p;
-      slot_c[base + e] = s_c[e];
+      if (whole) {
+        p /= fn;
+        out.counts[e] = s_c[e];
+        out.probs[e] = p;
+        dot += (float)s_c[e] / (fn * (float)k) * p;
+      } else {
+        slot_p[base + e] = p;
+        slot_c[base + e] = s_c[e];
+      }
+    }
+    if (whole) {
+      dot = wave_sum(dot);
+      if (lane == 0) s_w[wv] = dot;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 1; w < kWavesP; ++w) dot += s_w[w];
+        out.tokens[0] = s_n;
+        out.tokens[1] = s_n > 0;
+        *out.loss = s_n > 0 ? alpha * (float)E * dot : 0.f;
+      }
+      return;
     }
     if (tid == 0) slot_n[b + s] = s_n;
     __syncthreads();
@@ -274,23 +373,21 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
       __hip_atomic_store(&dots[blockIdx.x], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (ec == 0)
         __hip_atomic_store(&tokens[s], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __threadfence();
-      s_last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-               (int)gridDim.x - 1;
+      s_last = 1;
+      if (gridDim.x > 1) {
+        s_last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                 (int)gridDim.x - 1;
+      }
     }
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   float sum = 0.f;
   int some = 0;
-  for (int i = tid; i < S; i += kGroupsF * kWave) {
-    const int ns = __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (ns <= 0) continue;
-    ++some;
-    for (int j = 0; j < EC; ++j)
-      sum += __hip_atomic_load(&dots[i * EC + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  for (int i = tid; i < (int)gridDim.x; i += kGroupsF * kWave)  // (0 for an empty sequence)
+    sum += __hip_atomic_load(&dots[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = tid; i < S; i += kGroupsF * kWave)
+    some += __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
   sum = wave_sum(sum);
   for (int o = 32; o > 0; o >>= 1) some += __shfl_xor(some, o, kWave);
   if (lane == 0) {
@@ -313,124 +410,164 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
 // ---------------------------------------------------------------------------
 // gradient of the logits
 // ---------------------------------------------------------------------------
-template <int NP, bool VEC, bool RENORM>
+// The selected experts of one token, spread over its lanes: lane l holds
+// entries l, l + L, ... (k <= E <= V L, so at most V of them), -1 for none.
+template <class R, bool GATHER>
+struct Picked {
+  static constexpr int L = R::L, N = R::V < (MOE_MAX_TOPK + L - 1) / L ? R::V : (MOE_MAX_TOPK + L - 1) / L;
+  int e[N];
+  float d[N], z[GATHER ? N : 1];  // gradient of the weight; logit
+  __device__ __forceinline__ void load(const int32_t *idx, const float *dw, const float *row, int k,
+                                       int E, int l) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      const int j = c * L + l, jc = min(j, k - 1);
+      const int en = idx[jc];
+      const float dn = dw[jc];
+      const bool in = j < k && en >= 0 && en < E;
+      e[c] = in ? en : -1;
+      d[c] = in ? dn : 0.f;
+      if constexpr (GATHER) {
+        const float zn = row[in ? en : 0];
+        z[c] = in ? zn : -INFINITY;
+      }
+    }
+  }
+};
+
+// LDS operations of one wave, in program order for the compiler too
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <class R, bool RENORM>
 __global__ __launch_bounds__(256) void route_backward_kernel(
     const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
     const float *__restrict__ dw, const int32_t *__restrict__ counts,
     const int32_t *__restrict__ tokens, float alpha, const float *__restrict__ d_loss,
     const int32_t *__restrict__ off, const uint8_t *__restrict__ mask, int T, int E, int k, int S,
-    int C, int L, float *__restrict__ out) {
-  using R = Row<NP, VEC>;
-  constexpr int U = R::V <= 4 ? 2 : 1;
-  constexpr int NW = 256 / kWave;
+    int C, float *__restrict__ out) {
+  constexpr int U = R::V <= 4 ? 4 : (R::V <= 8 ? 2 : 1), L = R::L, nq = kWave / L, NW = 256 / kWave;
+  constexpr int step = NW * nq;
+  using P = Picked<R, RENORM>;
+  __shared__ __align__(16) float s_g[NW][U * kWave * R::V];
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
-  const int l = lane & (L - 1), q = lane / L, nq = kWave / L, step = NW * nq;
+  const int l = lane & (L - 1), q = lane / L;
   const int b0 = blockIdx.x * C, b1 = min(T, b0 + C);
   const int first = wv * nq + q;
-  R zero;
+  // the balance term's factor, looked up beside the first loads
+  const float some = counts ? (float)max(tokens[S], 1) : 1.f;
+  const float scale = counts ? (d_loss ? *d_loss : 1.f) * alpha * (float)E / some : 0.f;
+  const int s_first = off ? sequence_of(off, S, b0) : 0;
+  for (int t0 = b0 + first; t0 - q < b1; t0 += U * step) {
+    // every load of the batch first
+    R x[U];
+    P pick[U];
+    bool on[U];
 #pragma unroll
-  for (int i = 0; i < R::V; ++i) zero.v[i] = 0.f;
-  if (off) {  // rows outside every sequence
-    const int lo = off[0], hi = off[S];
-    for (int t = b0 + first; t < b1; t += step)
-      if (t < lo || t >= hi) zero.store(out + (size_t)t * E, l, L, E);
-  }
-  int s = off ? sequence_of(off, S, b0) : 0;
-  for (; s < S; ++s) {
-    const int lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
-    if (lo >= b1) break;
-    const int ta = max(lo, b0), tb = min(hi, b1);
-    if (ta >= tb) continue;
-    // b[e], the balance loss's derivative by p_t[e], the same for the whole
-    // sequence
-    float bal[R::V];
-#pragma unroll
-    for (int i = 0; i < R::V; ++i) bal[i] = 0.f;
-    if (counts) {
-      const float n = (float)max(tokens[s], 1), some = (float)max(tokens[S], 1);
-      const float coef = (d_loss ? *d_loss : 1.f) * alpha * (float)E / (some * n);
-#pragma unroll
-      for (int i = 0; i < R::V; ++i) {
-        const int e = R::expert(i, l, L);
-        if (e < E) bal[i] = coef * ((float)counts[(size_t)s * E + e] / (n * (float)k));
-      }
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * step, tc = min(t, b1 - 1);
+      on[u] = t < b1;
+      if (mask) on[u] = on[u] && mask[tc];
+      x[u].load(logits + (size_t)tc * E, l, E);
+      if (dw)
+        pick[u].load(topk_idx + (size_t)tc * k, dw + (size_t)tc * k, logits + (size_t)tc * E, k, E, l);
     }
-    for (int t0 = ta + first; t0 - q < tb; t0 += U * step) {
-      R x[U];
-      bool on[U], in[U];
+    R g[U];  // the gate's part: of p (raw), of the logits (renormalised)
+    if (dw) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        g[u].fill(0.f);
+        g[u].store(s_g[wv] + (u * nq + q) * (R::V * L), l, R::V * L);
+      }
+      wave_order();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (dw) {
+        if constexpr (RENORM) {
+          // q over the selected logits, shifted by their own maximum; d
+          // becomes the gradient of the entry's logit
+          float m = pick[u].z[0], z = 0.f, dot = 0.f;
+#pragma unroll
+          for (int c = 1; c < P::N; ++c) m = fmaxf(m, pick[u].z[c]);
+          m = lanes_max<L>(m);
+          if (m == -INFINITY) m = 0.f;
+#pragma unroll
+          for (int c = 0; c < P::N; ++c) {
+            pick[u].z[c] = exp_neg(pick[u].z[c] - m);
+            z += pick[u].z[c];
+            dot = fmaf(pick[u].z[c], pick[u].d[c], dot);
+          }
+          z = lanes_sum<L>(z);
+          const float inv = z != 0.f ? 1.f / z : 0.f;
+          dot = lanes_sum<L>(dot) * inv;
+#pragma unroll
+          for (int c = 0; c < P::N; ++c) pick[u].d[c] = pick[u].z[c] * inv * (pick[u].d[c] - dot);
+        }
+        // the entries meet their experts' lanes in the wave's own LDS (an
+        // expert that is there twice takes both)
+        float *sc = s_g[wv] + (u * nq + q) * (R::V * L);
+#pragma unroll
+        for (int c = 0; c < P::N; ++c)
+          if (pick[u].e[c] >= 0)
+            __hip_atomic_fetch_add(&sc[pick[u].e[c]], pick[u].d[c], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_WAVEFRONT);
+      }
+      softmax_row(x[u]);
+    }
+    if (dw) wave_order();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      g[u].fill(0.f);
+      if (dw) g[u].load(s_g[wv] + (u * nq + q) * (R::V * L), l, R::V * L);
+    }
+    // the batch's tokens sequence by sequence; b[e], the balance loss's
+    // derivative by p_t[e], is the same for a whole sequence
+    bool done[U] = {};
+    for (int s = s_first; s < S; ++s) {
+      const int lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
+      if (lo >= b1) break;
+      if (max(lo, b0) >= min(hi, b1)) continue;
+      R bal;
+      bal.fill(0.f);
+      if (counts) {
+        const float n = (float)max(tokens[s], 1);
+#pragma unroll
+        for (int i = 0; i < R::V; ++i) {
+          const int e = R::expert(i, l), c = counts[(size_t)s * E + min(e, E - 1)];
+          bal.v[i] = e < E ? scale / n * ((float)c / (n * (float)k)) : 0.f;
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * step;
-        in[u] = t < tb;
-        on[u] = in[u] && (!mask || mask[t]);
-        if (on[u]) {
-          x[u].load(logits + (size_t)t * E, l, L, E);
-        } else {
-#pragma unroll
-          for (int i = 0; i < R::V; ++i) x[u].v[i] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const size_t t = (size_t)(t0 + u * step);
-        float g[R::V];
-#pragma unroll
-        for (int i = 0; i < R::V; ++i) g[i] = bal[i];
-        float add[RENORM ? R::V : 1];
-        if (RENORM) {
-#pragma unroll
-          for (int i = 0; i < (RENORM ? R::V : 1); ++i) add[i] = 0.f;
-        }
-        if (dw && on[u]) {
-          if (RENORM) {
-            // q over the selected logits, shifted by their own maximum
-            float m = -INFINITY, z = 0.f, dot = 0.f;
-            for (int j = 0; j < k; ++j) {
-              const int e = topk_idx[t * k + j];
-              if (e >= 0 && e < E) m = fmaxf(m, logits[t * E + e]);
-            }
-            if (m == -INFINITY) m = 0.f;
-            for (int j = 0; j < k; ++j) {
-              const int e = topk_idx[t * k + j];
-              if (e < 0 || e >= E) continue;
-              const float w = exp_neg(logits[t * E + e] - m);
-              z += w;
-              dot = fmaf(w, dw[t * k + j], dot);
-            }
-            const float inv = z != 0.f ? 1.f / z : 0.f;
-            dot *= inv;
-            for (int j = 0; j < k; ++j) {
-              const int e = topk_idx[t * k + j];
-              if (e < 0 || e >= E) continue;
-              const float part = exp_neg(logits[t * E + e] - m) * inv * (dw[t * k + j] - dot);
-#pragma unroll
-              for (int i = 0; i < (RENORM ? R::V : 1); ++i)
-                add[i] += R::expert(i, l, L) == e ? part : 0.f;
-            }
-          } else {
-            for (int j = 0; j < k; ++j) {
-              const int e = topk_idx[t * k + j];
-              const float d = dw[t * k + j];
-#pragma unroll
-              for (int i = 0; i < R::V; ++i) g[i] += R::expert(i, l, L) == e ? d : 0.f;
-            }
-          }
-        }
-        softmax_row(x[u], L);
+        const bool mine = on[u] && t >= lo && t < hi;
         float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < R::V; ++i) dot = fmaf(x[u].v[i], g[i], dot);
-        dot = lanes_sum(dot, L);
         R r;
 #pragma unroll
         for (int i = 0; i < R::V; ++i) {
-          r.v[i] = x[u].v[i] * (g[i] - dot);
-          if (RENORM) r.v[i] += add[RENORM ? i : 0];
-          if (!on[u]) r.v[i] = 0.f;
+          r.v[i] = RENORM ? bal.v[i] : bal.v[i] + g[u].v[i];
+          dot = fmaf(x[u].v[i], r.v[i], dot);
         }
-        if (in[u]) r.store(out + t * E, l, L, E);
+        dot = lanes_sum<L>(dot);
+#pragma unroll
+        for (int i = 0; i < R::V; ++i) {
+          r.v[i] = x[u].v[i] * (r.v[i] - dot);
+          if constexpr (RENORM) r.v[i] += g[u].v[i];
+        }
+        if (mine) {
+          r.store(out + (size_t)t * E, l, E);
+          done[u] = true;
+        }
       }
     }
+    R zero;  // tokens that take no part
+    zero.fill(0.f);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t0 + u * step < b1 && !done[u]) zero.store(out + (size_t)(t0 + u * step) * E, l, E);
   }
 }
 
@@ -442,12 +579,56 @@ int lanes_for(int E) {
   return L;
 }
 
-// tokens per block of the loss's first launch: 16 (as many workgroups as a
-// small batch can give), doubled while more than 512 blocks remain (two per
-// CU), so that the slots stay a small share of the logits' bytes
-int loss_block(int T) {
-  int C = 16;
-  while ((T + C - 1) / C > 512 && C < 1024) C <<= 1;
+// f(Row) with the compiled row shape for E experts
+template <int NP, bool VEC, class F>
+void with_lanes(int L, F f) {
+  switch (L) {
+    case 1: f(Row<1, NP, VEC>()); break;
+    case 2: f(Row<2, NP, VEC>()); break;
+    case 4: f(Row<4, NP, VEC>()); break;
+    case 8: f(Row<8, NP, VEC>()); break;
+    case 16: f(Row<16, NP, VEC>()); break;
+    case 32: f(Row<32, NP, VEC>()); break;
+    default: f(Row<64, NP, VEC>()); break;
+  }
+}
+template <class F>
+void with_row(int E, F f) {
+  const int L = lanes_for(E);
+  if (E % 4 == 0) {
+    const int np = (E / 4 + L - 1) / L;
+    if (np <= 1) with_lanes<1, true>(L, f);
+    else if (np <= 2) f(Row<64, 2, true>());
+    else f(Row<64, 4, true>());
+  } else {
+    const int np = (E + L - 1) / L;
+    if (np <= 1) with_lanes<1, false>(L, f);
+    else if (np <= 2) f(Row<64, 2, false>());
+    else if (np <= 4) f(Row<64, 4, false>());
+    else if (np <= 8) f(Row<64, 8, false>());
+    else f(Row<64, 16, false>());
+  }
+}
+
+// token slots of a workgroup of the loss's first launch times tokens in flight
+int loss_batch(int E) {
+  int n = 0;
+  with_row(E, [&](auto row) {
+    using R = decltype(row);
+    n = unroll_of<R>() * kWavesP * (kWave / R::L);
+  });
+  return n;
+}
+
+// Tokens per block of the loss's first launch.  A small batch is one block
+// (a workgroup's loads of a few thousand values cost less than a second
+// launch); otherwise one batch of the workgroup's token slots (the most that
+// is in flight at once), halved down to 16 while there are fewer than 512
+// blocks (two per CU).
+int loss_block(int T, int E, int S, int batch) {
+  if (S == 1 && (long long)T * E <= 16384) return T > 0 ? T : 1;
+  int C = batch > 16 ? batch : 16;
+  while (C > 16 && (T + C - 1) / C < 512) C >>= 1;
   return C;
 }
 
@@ -456,7 +637,7 @@ struct LossWs {
 };
 
 LossWs loss_ws(int T, int E, int S) {
-  const int C = loss_block(T), EC = (E + kWave - 1) / kWave;
+  const int C = loss_block(T, E, S, loss_batch(E)), EC = (E + kWave - 1) / kWave;
   const size_t slots = (size_t)((T + C - 1) / C) + S;
   LossWs w;
   w.p = 0;
@@ -468,42 +649,6 @@ LossWs loss_ws(int T, int E, int S) {
   return w;
 }
 
-// the compiled row shape for E experts on L lanes: f(Row<NP, VEC>())
-template <class F>
-void with_row(int E, int L, F f) {
-  if (E % 4 == 0) {
-    const int np = (E / 4 + L - 1) / L;
-    if (np <= 1) f(Row<1, true>());
-    else if (np <= 2) f(Row<2, true>());
-    else f(Row<4, true>());
-  } else {
-    const int np = (E + L - 1) / L;
-    if (np <= 1) f(Row<1, false>());
-    else if (np <= 2) f(Row<2, false>());
-    else if (np <= 4) f(Row<4, false>());
-    else if (np <= 8) f(Row<8, false>());
-    else f(Row<16, false>());
-  }
-}
-
-template <int NP, bool VEC>
-void launch_partial(Row<NP, VEC>, int blocks, hipStream_t st, const float *logits,
-                    const int32_t *idx, const int32_t *off, const uint8_t *mask, int T, int E,
-                    int k, int S, int C, int L, float *p, int32_t *c, int32_t *n, int32_t *ticket) {
-  hipLaunchKernelGGL((balance_partial_kernel<NP, VEC>), dim3(blocks), dim3(kThreadsP), 0, st, logits,
-                     idx, off, mask, T, E, k, S, C, L, p, c, n, ticket);
-}
-
-template <bool RENORM, int NP, bool VEC>
-void launch_backward(Row<NP, VEC>, int blocks, hipStream_t st, const float *logits,
-                     const int32_t *idx, const float *dw, const int32_t *counts,
-                     const int32_t *tokens, float alpha, const float *d_loss, const int32_t *off,
-                     const uint8_t *mask, int T, int E, int k, int S, int C, int L, float *out) {
-  hipLaunchKernelGGL((route_backward_kernel<NP, VEC, RENORM>), dim3(blocks), dim3(256), 0, st,
-                     logits, idx, dw, counts, tokens, alpha, d_loss, off, mask, T, E, k, S, C, L,
-                     out);
-}
-
 }  // namespace
 
 size_t balance_loss_ws_bytes(int T, int E, int S) { return loss_ws(T, E, S).bytes; }
@@ -512,20 +657,23 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *topk_idx, con
                                const uint8_t *mask, int T, int E, int k, int S, float alpha,
                                int32_t *counts, float *probs, int32_t *tokens, float *loss, void *ws,
                                hipStream_t s) {
-  const int C = loss_block(T), EC = (E + kWave - 1) / kWave, L = lanes_for(E);
+  const int C = loss_block(T, E, S, loss_batch(E)), EC = (E + kWave - 1) / kWave;
   const LossWs w = loss_ws(T, E, S);
   char *base = static_cast<char *>(ws);
   float *p = reinterpret_cast<float *>(base + w.p);
   int32_t *c = reinterpret_cast<int32_t *>(base + w.c), *n = reinterpret_cast<int32_t *>(base + w.n);
   float *dots = reinterpret_cast<float *>(base + w.dots);
   int32_t *ticket = reinterpret_cast<int32_t *>(base + w.ticket);
-  with_row(E, L, [&](auto row) {
-    // (one block for an empty batch: it clears the ticket)
-    launch_partial(row, max(1, (T + C - 1) / C), s, logits, topk_idx, off, mask, T, E, k, S, C, L, p, c, n,
-                   ticket);
+  // (one block for an empty batch too)
+  const int blocks = max(1, (T + C - 1) / C);
+  const LossOut out = {counts, probs, tokens, loss};
+  with_row(E, [&](auto row) {
+    hipLaunchKernelGGL((balance_partial_kernel<decltype(row)>), dim3(blocks), dim3(kThreadsP), 0, s,
+                       logits, topk_idx, off, mask, T, E, k, S, C, alpha, p, c, n, ticket, out);
   });
-  hipLaunchKernelGGL(balance_final_kernel, dim3(S * EC), dim3(kGroupsF * kWave), 0, s, p, c, n, off,
-                     T, E, k, S, C, EC, alpha, counts, probs, tokens, loss, dots, ticket);
+  if (blocks > 1 || S > 1)
+    hipLaunchKernelGGL(balance_final_kernel, dim3(S * EC), dim3(kGroupsF * kWave), 0, s, p, c, n, off,
+                       T, E, k, S, C, EC, alpha, counts, probs, tokens, loss, dots, ticket);
   return hipGetLastError();
 }
 
@@ -534,16 +682,17 @@ hipError_t launch_route_backward(const float *logits, const int32_t *topk_idx, c
                                  float alpha, const float *d_loss, const int32_t *off,
                                  const uint8_t *mask, int T, int E, int k, int S, float *d_logits,
                                  hipStream_t s) {
-  const int L = lanes_for(E);
-  // tokens per workgroup: two passes of its token slots, at least 16
-  const int C = max(16, 2 * (256 / kWave) * (kWave / L));
-  with_row(E, L, [&](auto row) {
+  with_row(E, [&](auto row) {
+    using R = decltype(row);
+    // tokens per workgroup: one batch of its token slots, at least 16
+    const int C = max(16, (R::V <= 4 ? 4 : 2) * (256 / R::L));
+    const dim3 grid((T + C - 1) / C), block(256);
     if (renorm)
-      launch_backward<true>(row, (T + C - 1) / C, s, logits, topk_idx, dw, counts, tokens, alpha,
-                            d_loss, off, mask, T, E, k, S, C, L, d_logits);
+      hipLaunchKernelGGL((route_backward_kernel<R, true>), grid, block, 0, s, logits, topk_idx, dw,
+                         counts, tokens, alpha, d_loss, off, mask, T, E, k, S, C, d_logits);
     else
-      launch_backward<false>(row, (T + C - 1) / C, s, logits, topk_idx, dw, counts, tokens, alpha,
-                             d_loss, off, mask, T, E, k, S, C, L, d_logits);
+      hipLaunchKernelGGL((route_backward_kernel<R, false>), grid, block, 0, s, logits, topk_idx, dw,
+                         counts, tokens, alpha, d_loss, off, mask, T, E, k, S, C, d_logits);
   });
   return hipGetLastError();
 }
