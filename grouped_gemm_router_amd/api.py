@@ -375,6 +375,12 @@ def _arg(t, name, dtype, *shape, device):
     dtype[shape] on the GPU `device` (an index)."""
     if t is None:
         return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == device):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor, got %r" % (name, type(t)))
     if t.dtype != dtype:
@@ -383,9 +389,15 @@ def _arg(t, name, dtype, *shape, device):
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.get_device() != device:
-        raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
-    return t.data_ptr()
+    raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
+
+
+def _raw_stream(stream, device) -> int:
+    """The hipStream_t of a stream, or of the device's current stream (read
+    without making a torch.cuda.Stream object of it)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _gpu(t, name):
@@ -467,7 +479,7 @@ def moe_balance_loss(logits, topk_idx, counts, probs, tokens, loss, *, alpha=0.0
                    _arg(probs, "probs", f32, S, E, device=dev),
                    _arg(tokens, "tokens", i32, S + 1, device=dev),
                    _arg(loss, "loss", f32, 1, device=dev), ws.data_ptr(), ws_bytes,
-                   _stream(stream))
+                   _raw_stream(stream, dev))
 
 
 def moe_route_backward(logits, topk_idx, d_logits, *, d_topk_w=None, flags=0, counts=None,
@@ -489,7 +501,7 @@ def moe_route_backward(logits, topk_idx, d_logits, *, d_topk_w=None, flags=0, co
                    _arg(counts, "counts", i32, S, E, device=dev),
                    _arg(tokens, "tokens", i32, S + 1, device=dev), float(alpha),
                    _arg(d_loss, "d_loss", f32, 1, device=dev), off, mask, T, E, k, S,
-                   _arg(d_logits, "d_logits", f32, T, E, device=dev), _stream(stream))
+                   _arg(d_logits, "d_logits", f32, T, E, device=dev), _raw_stream(stream, dev))
 
 
 def _lora_dt(dtype) -> int:
@@ -526,7 +538,7 @@ def moe_lora_linear(x, A, B, scale, adapter, y, v, *, W=None, ws=None, stream=No
                    _lora_dt(dt), _arg(scale, "scale", f32, n, device=dev),
                    _arg(adapter, "adapter", torch.int32, T, device=dev), T, N, K, r, n,
                    _arg(y, "y", y.dtype, T, N, device=dev), _lora_dt(y.dtype),
-                   _arg(v, "v", f32, T, r, device=dev), ws.data_ptr(), ws_bytes, _stream(stream))
+                   _arg(v, "v", f32, T, r, device=dev), ws.data_ptr(), ws_bytes, _raw_stream(stream, dev))
 
 
 def moe_lora_backward_workspace_size(T: int, N: int, K: int, r: int, n: int, dtype) -> int:
@@ -557,4 +569,4 @@ def moe_lora_linear_backward(dy, x, A, B, scale, adapter, v, u, *, W_t=None, dx=
                    _arg(u, "u", f32, T, r, device=dev), _arg(dx, "dx", dt, T, K, device=dev),
                    _arg(dA, "dA", f32, n, r, K, device=dev),
                    _arg(dB, "dB", f32, n, r, N, device=dev), ws.data_ptr(), ws_bytes,
-                   _stream(stream))
+                   _raw_stream(stream, dev))

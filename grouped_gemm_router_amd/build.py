@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["moe_api.hip", "route.hip", "permute.hip", "gemm_bf16.hip", "gemm_fp8.hip", "gemm_fp8_ring.hip",
            "gemm_simple.hip", "combine.hip", "quant.hip", "router_stats.hip", "balance.hip",
-           "lora_shrink.hip", "lora_expand.hip", "lora_wgrad.hip"]
+           "lora_plan.hip", "lora_shrink.hip", "lora_expand.hip", "lora_wgrad.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -5,13 +5,13 @@
 // starts.  Fusing its product with F into the projection writes y once, with
 // one rounding, where a second pass would read and write it again.
 //
-// The low-rank part of a 32-row block that belongs to one adapter (a prompt's
-// rows) goes through the matrix cores: v is split into bf16 terms (two for
-// a bf16 y, three for an fp32 y, so that the product keeps 16 or 24 bits of
-// v) and multiplied like 16 more columns of x.  In any other block every row
-// reads its own adapter's rows of F on the vector ALUs.  No row ever meets
-// another adapter's values, not even multiplied by zero: an infinity in one
-// request's adapter stays in that request's rows.
+// The low-rank part of a 32-row block of one or a few adapters (rows come
+// sorted by adapter) goes through the matrix cores: v is split into bf16
+// terms (two for a bf16 y, three for an fp32 y, so that the product keeps 16
+// or 24 bits of v) and multiplied like 16 more columns of x.  In a block of
+// many adapters every row reads its own adapter's rows of F on the vector
+// ALUs.  No row ever adds another adapter's values, not even multiplied by
+// zero: an infinity in one request's adapter stays in that request's rows.
 #include "gemm_bf16_tile.h"
 #include "lora_internal.h"
 
@@ -91,16 +91,51 @@ __device__ __forceinline__ void load_ranks(uint16_t (&w)[NB][8], const uint16_t 
     for (int i = 0; i < 8; ++i) w[nb][i] = F[(size_t)i * N + n[nb]];
 }
 
-// The low-rank part of a wave's MI x NB blocks, for the row blocks whose 32
-// rows share an adapter: acc[i][nb] += v F, 16 ranks a step; s_hom says which
-// blocks do.  s_ad: the tile's adapters (-1 for none); first: the wave's first
-// row block; n0: its first column.
+// acc[nb] += v F of 32 rows, 16 ranks from j0: the lane's eight values of v
+// (zero where its ranks do not exist), split into TERMS, and its columns'
+// ranks w.
+template <int TERMS, int NB>
+__device__ __forceinline__ void mma_ranks(f32x16 (&acc)[NB], f32x4 v0, f32x4 v1,
+                                          const uint16_t (&w)[NB][8], bool in) {
+  float f[8];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f[c] = in ? v0[c] : 0.f;
+    f[4 + c] = in ? v1[c] : 0.f;
+  }
+  bf16x8 va[TERMS];
+  split_bf16<TERMS>(f, va);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    u32x4 q;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      q[c] = in ? (uint32_t)w[nb][2 * c] | ((uint32_t)w[nb][2 * c + 1] << 16) : 0u;
+    const bf16x8 b = __builtin_bit_cast(bf16x8, q);
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+      acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[k], b, acc[nb], 0, 0, 0);
+  }
+}
+
+// Adapters among 32 rows up to which they go through the matrix cores one
+// after the other.
+constexpr int kBlockKinds = 6;
+
+// The low-rank part of a wave's MI x NB blocks on the matrix cores, 16 ranks
+// a step; s_hom says for which blocks it is done here.
+//   * a block whose 32 rows share an adapter: acc[i][nb] += v F;
+//   * a block of a few adapters: all 32 rows times each adapter's factor into
+//     registers of their own, of which each row adds its own adapter's.
+// s_row, s_ad: the tile's rows and adapters (-1 for none); first: the wave's
+// first row block; n0: its first column.
 template <int TERMS, int MI, int NB>
-__device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int *s_ad, int *s_hom,
-                                                int first, bool tell, int m0, int n0, const char *F,
-                                                const float *v, int T, int N, int r, int fr, int fh) {
+__device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int *s_row,
+                                                const int *s_ad, int *s_hom, int first, bool tell,
+                                                int n0, const char *F, const float *v, int N, int r,
+                                                int fr, int fh) {
   int a[MI];
-  bool hom[MI], any = false;
+  bool hom[MI], few[MI], any = false;
   const float *vr[MI];
   int n[NB];
 #pragma unroll
@@ -111,15 +146,18 @@ __device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int
     const int a0 = __builtin_amdgcn_readfirstlane(mine);
     hom[i] = a0 >= 0 && __all(mine == a0);
     a[i] = max(a0, 0);
-    vr[i] = v + (size_t)min(m0 + row, T - 1) * r;
+    vr[i] = v + (size_t)s_row[row] * r;
     any = any || hom[i];
-    if (tell) s_hom[first + i] = hom[i];
+    int kinds = 0;
+    for (unsigned left = (unsigned)__ballot(mine >= 0); left; ++kinds)
+      left &= ~(unsigned)__ballot(mine == __builtin_amdgcn_readlane(mine, __builtin_ctz(left)));
+    few[i] = !hom[i] && kinds > 0 && kinds <= kBlockKinds;
+    if (tell) s_hom[first + i] = hom[i] || few[i];
   }
-  if (!any) return;
   const uint16_t *Fw = reinterpret_cast<const uint16_t *>(F);
-  for (int j0 = 0; j0 < r; j0 += 16) {
-    // r is a multiple of 8: a lane's eight ranks exist or not.  Where they
-    // do not, the last eight are loaded and both operands are zero.
+  // r is a multiple of 8: a lane's eight ranks of a step exist or not.  Where
+  // they do not, the last eight are loaded and both operands are zero.
+  for (int j0 = 0; any && j0 < r; j0 += 16) {
     const bool in = j0 + 8 * fh < r;
     const int j = min(j0 + 8 * fh, r - 8);
     f32x4 v0[MI], v1[MI];
@@ -134,25 +172,36 @@ __device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int
     for (int i = 0; i < MI; ++i) {
       // the rows of a prompt share the factor's fragments from block to block
       if (i > 0 && a[i] != a[i - 1]) load_ranks<NB>(w, Fw + ((size_t)a[i] * r + j) * N, N, n);
-      if (!hom[i]) continue;
-      float f[8];
+      if (hom[i]) mma_ranks<TERMS, NB>(acc[i], v0[i], v1[i], w, in);
+    }
+  }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f[c] = in ? v0[i][c] : 0.f;
-        f[4 + c] = in ? v1[i][c] : 0.f;
+  for (int i = 0; i < MI; ++i) {
+    if (!few[i]) continue;
+    const int mine = s_ad[(first + i) * 32 + fr];
+    unsigned todo = (unsigned)__ballot(mine >= 0);
+    while (todo) {
+      const int who = __builtin_amdgcn_readlane(mine, __builtin_ctz(todo));
+      const unsigned same = (unsigned)__ballot(mine == who);
+      todo &= ~same;
+      f32x16 own[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) own[nb] = f32x16{};
+      for (int j0 = 0; j0 < r; j0 += 16) {
+        const bool in = j0 + 8 * fh < r;
+        const int j = min(j0 + 8 * fh, r - 8);
+        uint16_t w[NB][8];
+        load_ranks<NB>(w, Fw + ((size_t)who * r + j) * N, N, n);
+        mma_ranks<TERMS, NB>(own, *reinterpret_cast<const f32x4 *>(vr[i] + j),
+                             *reinterpret_cast<const f32x4 *>(vr[i] + j + 4), w, in);
       }
-      bf16x8 va[TERMS];
-      split_bf16<TERMS>(f, va);
+      // register e holds row 8 (e / 4) + 4 fh + e % 4
+      const unsigned rows = same >> (4 * fh);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        u32x4 q;
+      for (int e = 0; e < 16; ++e) {
+        const bool takes = (rows >> (8 * (e >> 2) + (e & 3))) & 1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          q[c] = in ? (uint32_t)w[nb][2 * c] | ((uint32_t)w[nb][2 * c + 1] << 16) : 0u;
-        const bf16x8 b = __builtin_bit_cast(bf16x8, q);
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          acc[i][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[k], b, acc[i][nb], 0, 0, 0);
+        for (int nb = 0; nb < NB; ++nb) acc[i][nb][e] += takes ? own[nb][e] : 0.f;
       }
     }
   }
@@ -175,12 +224,24 @@ unsigned tile_grid(int MT, int NT) {
   return (unsigned)((major + 7) / 8 * 8) * (unsigned)minor;
 }
 
+// row i of a tile: where it lies in the batch (rows past T repeat the last
+// one) and its adapter, -1 for none
+__device__ __forceinline__ void load_row(int *s_row, int *s_ad, int i, int m0, const int32_t *adapter,
+                                         const int32_t *order, int T, int n) {
+  int t = min(m0 + i, T - 1);
+  if (order) t = order[t];
+  const int a = adapter[t];
+  s_row[i] = t;
+  s_ad[i] = a >= 0 && a < n ? a : -1;
+}
+
 // rows [32 blk, 32 blk + 32) of a tile, staged in fp32 with row pitch SP, for
 // WM row blocks at once (stage_of(w) holds tile row block first + w * stride):
 // add what is left of the low-rank part and of y, round, store 8-column pieces
 template <int ES, int OS, int BN, int SP, int WM, bool VEC, class StageOf>
 __device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int stride, int m0,
-                                              int n0, const int *s_ad, const int *s_hom, bool add_y,
+                                              int n0, const int *s_row, const int *s_ad, const int *s_hom,
+                                            bool add_y,
                                               const char *F, const float *v, int T, int N, int r,
                                               char *y) {
   constexpr int CG = BN / 8, P = 1;  // pieces that a thread has in hand at once
@@ -196,9 +257,9 @@ __device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int s
     for (int p = 0; p < P; ++p) {
       const int q = min(q0 + p * nt, WM * 32 * CG - 1);
       const int w = q / (32 * CG), rr = (q / CG) % 32, c = (q % CG) * 8;
-      const int blk = first + w * stride, row = blk * 32 + rr, t = m0 + row, col = n0 + c;
-      live[p] = q0 + p * nt < WM * 32 * CG && t < T && col < N;
-      const int tc = min(t, T - 1), cc = live[p] ? col : 0;  // addresses that exist
+      const int blk = first + w * stride, row = blk * 32 + rr, col = n0 + c;
+      live[p] = q0 + p * nt < WM * 32 * CG && m0 + row < T && col < N;
+      const int tc = s_row[row], cc = live[p] ? col : 0;  // addresses that exist
       have[p] = N - cc;
       at[p] = (size_t)tc * N + cc;
       const int a = s_ad[row];
@@ -263,14 +324,15 @@ __device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int s
 
 template <int ES, int OS, int BN, int SP, int WM, class StageOf>
 __device__ __forceinline__ void finish_rows(StageOf stage_of, int first, int stride, int m0, int n0,
-                                            const int *s_ad, const int *s_hom, bool add_y,
+                                            const int *s_row, const int *s_ad, const int *s_hom,
+                                            bool add_y,
                                             const char *F, const float *v, int T, int N, int r,
                                             char *y) {
   if (N % 8 == 0)  // rows of F and of y are then 16-byte aligned
-    finish_pieces<ES, OS, BN, SP, WM, true>(stage_of, first, stride, m0, n0, s_ad, s_hom, add_y, F, v,
+    finish_pieces<ES, OS, BN, SP, WM, true>(stage_of, first, stride, m0, n0, s_row, s_ad, s_hom, add_y, F, v,
                                             T, N, r, y);
   else
-    finish_pieces<ES, OS, BN, SP, WM, false>(stage_of, first, stride, m0, n0, s_ad, s_hom, add_y, F,
+    finish_pieces<ES, OS, BN, SP, WM, false>(stage_of, first, stride, m0, n0, s_row, s_ad, s_hom, add_y, F,
                                              v, T, N, r, y);
 }
 
@@ -283,23 +345,22 @@ __device__ __forceinline__ void finish_rows(StageOf stage_of, int first, int str
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void expand_f32_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
-    const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
-    int n, char *__restrict__ y, int MT, int NT) {
+    const float *__restrict__ v, const int32_t *__restrict__ adapter,
+    const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
+    int NT) {
   constexpr int BM = 64, BNF = 64, SP = BNF + 4, NLD = (BM + BNF) * 8 / 256;
   __shared__ u32x4 ring[2][(BM + BNF) * 8];
-  __shared__ int s_ad[BM];
+  __shared__ int s_row[BM], s_ad[BM];
   __shared__ int s_hom[BM / 32];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
   const int m0 = at.mt * BM, n0 = at.nt * BNF;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int wm = wv / 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
-  if (tid < BM) {
-    const int a = adapter[min(m0 + tid, T - 1)];
-    s_ad[tid] = a >= 0 && a < n ? a : -1;
-  }
+  if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   if (tid < BM / 32) s_hom[tid] = 0;
   f32x16 acc = f32x16{};
+  __syncthreads();
   if (W) {
     const int KP = K / 4, KT = (KP + 7) / 8;
     const u32x4 *src[NLD];
@@ -307,7 +368,7 @@ __global__ __launch_bounds__(256) void expand_f32_kernel(
     for (int i = 0; i < NLD; ++i) {
       const int row = (tid + 256 * i) >> 3;
       src[i] = row < BM
-                   ? reinterpret_cast<const u32x4 *>(x + (size_t)min(m0 + row, T - 1) * K * 4)
+                   ? reinterpret_cast<const u32x4 *>(x + (size_t)s_row[row] * K * 4)
                    : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * 4);
     }
     u32x4 reg[NLD];
@@ -349,8 +410,8 @@ __global__ __launch_bounds__(256) void expand_f32_kernel(
   for (int e = 0; e < 16; ++e)
     stage[(wm * 32 + 8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * 32 + fr] = acc[e];
   __syncthreads();
-  finish_rows<4, 4, BNF, SP, 2>([&](int w) { return stage + w * 32 * SP; }, 0, 1, m0, n0, s_ad,
-                                s_hom, W == nullptr, F, v, T, N, r, y);
+  finish_rows<4, 4, BNF, SP, 2>([&](int w) { return stage + w * 32 * SP; }, 0, 1, m0, n0, s_row,
+                                s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -365,8 +426,9 @@ __device__ u32x4 g_zero;
 template <int OS, int BM, int BNT, int WM, int WN, int NS>
 __global__ __launch_bounds__(256) void expand_ring_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
-    const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
-    int n, char *__restrict__ y, int MT, int NT, int rot) {
+    const float *__restrict__ v, const int32_t *__restrict__ adapter,
+    const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
+    int NT, int rot) {
   constexpr int MI = BM / WM / 32, NB = BNT / WN / 32;
   constexpr int IL = (BM + BNT) / 32;  // loads per wave and step
   constexpr int SLOT = (BM + BNT) * 8, SP = BNT + 4;
@@ -374,7 +436,7 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
   static_assert(32 * SP * 4 <= SLOT * 16 && WM <= 2, "a staged row block must fit a slot");
   static_assert(NS == 3 || NS == 4, "ring of three or four slots");
   __shared__ u32x4 s0[SLOT], s1[SLOT], s2[SLOT], s3[NS == 4 ? SLOT : 1];
-  __shared__ int s_ad[BM];
+  __shared__ int s_row[BM], s_ad[BM];
   __shared__ int s_hom[BM / 32];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
@@ -383,16 +445,14 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
             wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wv / WN, wn = wv % WN, fr = lane & 31, fh = lane >> 5;
 
-  if (tid < BM) {
-    const int a = adapter[min(m0 + tid, T - 1)];
-    s_ad[tid] = a >= 0 && a < n ? a : -1;
-  }
+  if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   f32x16 acc[MI][NB];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
 
+  __syncthreads();  // s_row
   if (W) {
     const int KP = K / 8, KT = (KP + 7) / 8, KF = KP / 8;  // steps, whole steps
     const int k_first = rot && KT == KF ? (int)(at.nt * 5u % (unsigned)KT) : 0;
@@ -404,7 +464,7 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
       const int sl = dma + i * 64 + lane, row = sl / 8;
       pc[i] = swzb(row, sl % 8);
       src[i] = (row < BM
-                    ? reinterpret_cast<const u32x4 *>(x + (size_t)min(m0 + row, T - 1) * K * 2)
+                    ? reinterpret_cast<const u32x4 *>(x + (size_t)s_row[row] * K * 2)
                     : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * 2)) +
                pc[i];
     }
@@ -484,10 +544,10 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 #undef MOE_READ
 #undef MOE_ISSUE
   }
-  __syncthreads();  // s_ad; every wave is done with the ring
+  __syncthreads();  // every wave is done with the ring
 
-  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_ad, s_hom, wm * MI, lane == 0 && wn == 0, m0,
-                                           n0 + wn * (NB * 32), F, v, T, N, r, fr, fh);
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_row, s_ad, s_hom, wm * MI, lane == 0 && wn == 0,
+                                           n0 + wn * (NB * 32), F, v, N, r, fr, fh);
   // 32 rows of every wave row at a time meet in LDS in fp32
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -501,7 +561,7 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
     __syncthreads();
     finish_rows<2, OS, BNT, SP, WM>(
         [&](int w) { return reinterpret_cast<const float *>(w == 0 ? s0 : s1); }, i, MI, m0, n0,
-        s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
+        s_row, s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
   }
 }
 
@@ -513,8 +573,9 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 template <int OS>
 __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
-    const float *__restrict__ v, const int32_t *__restrict__ adapter, int T, int N, int K, int r,
-    int n, char *__restrict__ y, int MT, int NT) {
+    const float *__restrict__ v, const int32_t *__restrict__ adapter,
+    const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
+    int NT) {
   constexpr int NW = 4, NWN = 2, MI = 4, NB = 4;
   constexpr int SLOTS_A2 = BM_MAX * PIECES_B;
   constexpr int IA = SLOTS_A2 / NW / 64, IB = SLOTS_B2 / NW / 64;
@@ -526,12 +587,16 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
   const int tid = threadIdx.x, lane = lane_id(),
             wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wv / NWN, wn = wv % NWN, fr = lane & 31, fh = lane >> 5;
+  // the tile's rows wait in the last B slot, which the K loop fills last
+  int *const rows = reinterpret_cast<int *>(sB2);
+  load_row(rows, rows + BM_MAX, tid, m0, adapter, order, T, n);
+  __syncthreads();
   const uint16_t *ga[IA], *gb[IB];
   const int dma_a = wv * (SLOTS_A2 / NW), dma_b = wv * (SLOTS_B2 / NW);
 #pragma unroll
   for (int i = 0; i < IA; ++i) {
     const int sl = dma_a + i * 64 + lane, row = sl / PIECES_B;
-    ga[i] = reinterpret_cast<const uint16_t *>(x) + (size_t)min(m0 + row, T - 1) * K +
+    ga[i] = reinterpret_cast<const uint16_t *>(x) + (size_t)rows[row] * K +
             swzb(row, sl % PIECES_B) * 8;
   }
 #pragma unroll
@@ -548,14 +613,12 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
   tile_k_loop<false, MI, NB, NWN, IA, IB>(acc, ga, gb, K / BK, dma_a, dma_b, wm, wn, fr, fh, MI, sA0,
                                           sA1, sB0, sB1, sB2);
   __syncthreads();  // every wave is done with the rings
-  int *const s_ad = reinterpret_cast<int *>(sA0), *const s_hom = s_ad + BM_MAX;
-  {
-    const int a = adapter[min(m0 + tid, T - 1)];
-    s_ad[tid] = a >= 0 && a < n ? a : -1;
-  }
+  int *const s_row = reinterpret_cast<int *>(sA0), *const s_ad = s_row + BM_MAX,
+             *const s_hom = s_ad + BM_MAX;
+  load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   __syncthreads();
-  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_ad, s_hom, wm * MI, lane == 0 && wn == 0, m0,
-                                           n0 + wn * (NB * 32), F, v, T, N, r, fr, fh);
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_row, s_ad, s_hom, wm * MI, lane == 0 && wn == 0,
+                                           n0 + wn * (NB * 32), F, v, N, r, fr, fh);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     // 32 rows of both wave rows: 32 x 256 fp32 are one B slot
@@ -569,7 +632,7 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     __syncthreads();
     finish_rows<2, OS, BN, BN, 2>(
         [&](int w) { return reinterpret_cast<const float *>(w == 0 ? sB0 : sB1); }, i, MI, m0, n0,
-        s_ad, s_hom, false, F, v, T, N, r, y);
+        s_row, s_ad, s_hom, false, F, v, T, N, r, y);
   }
 }
 
@@ -695,17 +758,17 @@ int pick_tile(int T, int N, int K, bool with_w, int cus) {
 
 template <class Kernel, class... More>
 void launch_tiles(Kernel kernel, int BM, int BNT, const char *x, const char *W, int ldw,
-                  const char *F, const float *v, const int32_t *adapter, int T, int N, int K, int r,
-                  int n, char *y, hipStream_t s, More... more) {
+                  const char *F, const float *v, const int32_t *adapter, const int32_t *order, int T,
+                  int N, int K, int r, int n, char *y, hipStream_t s, More... more) {
   const int MT = (T + BM - 1) / BM, NT = (N + BNT - 1) / BNT;
-  hipLaunchKernelGGL(kernel, dim3(tile_grid(MT, NT)), dim3(256), 0, s, x, W, ldw, F, v, adapter, T,
-                     N, K, r, n, y, MT, NT, more...);
+  hipLaunchKernelGGL(kernel, dim3(tile_grid(MT, NT)), dim3(256), 0, s, x, W, ldw, F, v, adapter,
+                     order, T, N, K, r, n, y, MT, NT, more...);
 }
 
 template <int OS>
 void launch_bf16(const char *x, const char *W, int ldw, const char *F, const float *v,
-                 const int32_t *adapter, int T, int N, int K, int r, int n, char *y, int cus,
-                 hipStream_t s) {
+                 const int32_t *adapter, const int32_t *order, int T, int N, int K, int r, int n,
+                 char *y, int cus, hipStream_t s) {
   if (W && T <= kExpandRowsMax) {
     const dim3 grid((N + 15) / 16), block(kRowWaves * kWave);
 #define MOE_ROWS(MB)                                                                             \
@@ -719,10 +782,11 @@ void launch_bf16(const char *x, const char *W, int ldw, const char *F, const flo
   }
   const int rot = T <= 128;
 #define MOE_TILES(kernel, BM, BNT) \
-  launch_tiles(kernel, BM, BNT, x, W, ldw, F, v, adapter, T, N, K, r, n, y, s, rot)
+  launch_tiles(kernel, BM, BNT, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y, s, rot)
   switch (pick_tile(T, N, K, W != nullptr, cus)) {
     case 0:
-      launch_tiles(expand_big_kernel<OS>, 256, 256, x, W, ldw, F, v, adapter, T, N, K, r, n, y, s);
+      launch_tiles(expand_big_kernel<OS>, 256, 256, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y,
+                   s);
       break;
     case 1: MOE_TILES((expand_ring_kernel<OS, 128, 128, 2, 2, 4>), 128, 128); break;
     case 2: MOE_TILES((expand_ring_kernel<OS, 64, 128, 1, 4, 4>), 64, 128); break;
@@ -734,16 +798,17 @@ void launch_bf16(const char *x, const char *W, int ldw, const char *F, const flo
 }  // namespace
 
 hipError_t launch_lora_expand(const void *x, const void *W, int ldw, const void *F, int dt,
-                              const float *v, const int32_t *adapter, int T, int N, int K, int r,
-                              int n, void *y, int y_dt, int cus, hipStream_t s) {
+                              const float *v, const int32_t *adapter, const int32_t *order, int T,
+                              int N, int K, int r, int n, void *y, int y_dt, int cus,
+                              hipStream_t s) {
   const char *xb = static_cast<const char *>(x), *wb = static_cast<const char *>(W),
              *fb = static_cast<const char *>(F);
   char *yb = static_cast<char *>(y);
   if (dt == MOE_F32)
-    launch_tiles(expand_f32_kernel, 64, 64, xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, s);
+    launch_tiles(expand_f32_kernel, 64, 64, xb, wb, ldw, fb, v, adapter, order, T, N, K, r, n, yb, s);
   else if (y_dt == MOE_F32)
-    launch_bf16<4>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
+    launch_bf16<4>(xb, wb, ldw, fb, v, adapter, order, T, N, K, r, n, yb, cus, s);
   else
-    launch_bf16<2>(xb, wb, ldw, fb, v, adapter, T, N, K, r, n, yb, cus, s);
+    launch_bf16<2>(xb, wb, ldw, fb, v, adapter, order, T, N, K, r, n, yb, cus, s);
   return hipGetLastError();
 }

@@ -7,8 +7,8 @@
 
 namespace moe {
 
-// rows up to which the shrink runs one wave per (row, rank)
-constexpr int kShrinkRowMax = 128;
+// rows of a tile of the sorted shrink, and the most slices that it cuts K into
+constexpr int kShrinkTile = 64, kShrinkSlices = 8;
 
 // Piece p of a row of np pieces, zero behind the row's end.  The load itself is
 // unconditional: under a condition, each load of a batch gets its own branch
@@ -39,16 +39,75 @@ __device__ __forceinline__ void split_bf16(const float (&f)[8], bf16x8 (&t)[TERM
 
 }  // namespace moe
 
+// One run of an adapter's rows in the plan's order: the backward pass's work
+// item.  slot < 0: the adapter's only unit.
+struct LoraUnit {
+  int adapter, pos, count, slot;
+};
+
+// Slices of K that the sorted shrink cuts a tile into: enough workgroups for
+// two per CU, at least 1 KB of every row each.
+inline int lora_shrink_slices(int T, int row_bytes, int r) {
+  const int tiles = (T + moe::kShrinkTile - 1) / moe::kShrinkTile * (r > 64 ? 2 : 1);
+  int s = 1;
+  while (s < moe::kShrinkSlices && tiles * s < 512 && row_bytes / (2 * s) >= 1024) s *= 2;
+  return s;
+}
+
+// Where the plan of a batch lies in a workspace, and the size of its units.
+// starts, tiles [n + 2]: each adapter's first row in the order and first
+// shrink tile, then those of the rows without an adapter, then the ends;
+// part: the slices of the shrink's tiles.
+struct LoraPlan {
+  size_t order, starts, tiles, units, adapters, n_units, part, bytes;
+  int TS, max_units, max_tiles;
+};
+
+// rows per unit: at most 64 slices to add; batches of up to 1024 rows are
+// never sliced and need no launch that adds slices
+inline LoraPlan lora_plan(int T, int N, int K, int r, int n, int es, bool backward) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  LoraPlan p;
+  const int by = ((T + 31) / 32 + 31) / 32 * 32;
+  p.TS = by > 1024 ? by : 1024;
+  p.max_units = T / p.TS + n;  // (an adapter without rows has one of no rows)
+  p.max_tiles = T / moe::kShrinkTile + (n + 1 < T ? n + 1 : T);
+  p.order = 0;
+  p.starts = up((size_t)T * 4);
+  p.tiles = p.starts + up((size_t)(n + 2) * 4);
+  p.units = p.tiles + up((size_t)(n + 2) * 4);
+  p.adapters = p.units + (backward ? up((size_t)p.max_units * sizeof(LoraUnit)) : 0);
+  p.n_units = p.adapters + (backward ? up((size_t)n * 8) : 0);
+  p.part = p.n_units + (backward ? 256 : 0);
+  const int slices = lora_shrink_slices(T, (backward ? N : K) * es, r);
+  const int RP = r <= 16 ? 16 : r <= 32 ? 32 : 64;
+  const size_t sums = (size_t)p.max_tiles * (r > 64 ? 2 : 1) * slices * moe::kShrinkTile * RP;
+  p.bytes = p.part + up(slices > 1 ? sums * 4 : 0);
+  return p;
+}
+
+// Whether the forward pass reads its rows through a plan: not where reading
+// every row's factors (the most that unsorted rows can cost, at some 5 bytes
+// a ps) takes less than the plan's launch and the longer way through it.
+inline bool lora_sorts(int T, int N, int K, int r, int es) {
+  return (double)T * r * ((double)N + K) * es > 128e6;
+}
+
+hipError_t launch_lora_plan(const int32_t *adapter, int T, int n, const LoraPlan &p, bool units,
+                            char *ws, hipStream_t s);
+
+// p: the plan in ws, or null (rows as they come)
 hipError_t launch_lora_shrink(const void *x, const void *F, int dt, const float *scale,
-                              const int32_t *adapter, int T, int K, int r, int n, float *v,
-                              hipStream_t s);
+                              const int32_t *adapter, const LoraPlan *p, char *ws, int T, int K,
+                              int r, int n, float *v, hipStream_t s);
 
 // y (+)= x W^T + v F: W null adds to y
 hipError_t launch_lora_expand(const void *x, const void *W, int ldw, const void *F, int dt,
-                              const float *v, const int32_t *adapter, int T, int N, int K, int r,
-                              int n, void *y, int y_dt, int cus, hipStream_t s);
+                              const float *v, const int32_t *adapter, const int32_t *order, int T,
+                              int N, int K, int r, int n, void *y, int y_dt, int cus, hipStream_t s);
 
-size_t lora_wgrad_ws_bytes(int T, int N, int K, int r, int n);
+// the plan (with its units), then the slices of adapters of several units
+size_t lora_wgrad_ws_bytes(int T, int N, int K, int r, int n, int es);
 hipError_t launch_lora_wgrad(const void *dy, const void *x, int dt, const float *u, const float *v,
-                             const int32_t *adapter, int T, int N, int K, int r, int n, float *dA,
-                             float *dB, void *ws, hipStream_t s);
+                             int T, int N, int K, int r, int n, float *dA, float *dB, void *ws,
+                             hipStream_t s);

@@ -1,0 +1,157 @@
+// lora_plan.hip -- the rows of a batch sorted by adapter.
+//
+// The adapters' products are fast where neighbouring rows share a factor.
+// One workgroup sorts the rows by adapter (stably, so that every sum over
+// rows has a fixed order; rows without an adapter come last) and, for the
+// backward pass, cuts each adapter's rows into units of at most TS.  The
+// other launches then read rows through this order, so a batch whose rows
+// come in any order costs what a batch of whole prompts costs.  Latency-bound:
+// a few dependent loads and scans.
+#include "lora_internal.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kPlanWaves = 16;
+constexpr int kBuckets = MOE_LORA_MAX_ADAPTERS + 1;
+
+// exclusive scans of four values over the workgroup's threads; *total: the sums
+struct Four {
+  int v[4];
+};
+__device__ __forceinline__ Four block_scan(Four x, Four *s_w, Four *total) {
+  const int wv = threadIdx.x / kWave;
+  Four ex, sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ex.v[i] = wave_exclusive_scan(x.v[i], &sum.v[i]);
+  if (lane_id() == 0) s_w[wv] = sum;
+  __syncthreads();
+  *total = Four{};
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    const Four q = s_w[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ex.v[i] += w < wv ? q.v[i] : 0;
+      total->v[i] += q.v[i];
+    }
+  }
+  return ex;
+}
+
+// One workgroup.  Wave w takes the w-th sixteenth of the rows; count[w][a]
+// becomes the place of its next row of adapter a (a == n: no adapter).
+// units == nullptr: the order only.
+__global__ __launch_bounds__(kPlanWaves *kWave) void lora_plan_kernel(
+    const int32_t *__restrict__ adapter, int T, int n, int TS, int32_t *__restrict__ order,
+    int32_t *__restrict__ starts, int32_t *__restrict__ tiles, LoraUnit *__restrict__ units,
+    int2 *__restrict__ adapters, int32_t *__restrict__ n_units) {
+  __shared__ int count[kPlanWaves][kBuckets];
+  __shared__ Four s_w[kPlanWaves];
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  const int chunk = ((T + kPlanWaves - 1) / kPlanWaves + kWave - 1) / kWave * kWave;
+  const long long c0 = (long long)wv * chunk;
+  const int t0 = (int)min(c0, (long long)T), t1 = (int)min(c0 + chunk, (long long)T);
+  // the first rows' adapters stay in registers for both passes
+  constexpr int KEEP = 8;
+  int mine[KEEP];
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int t = t0 + i * kWave + lane;
+    const int a = T > 0 ? adapter[min(t, T - 1)] : -1;
+    mine[i] = t < t1 ? (a >= 0 && a < n ? a : n) : -1;
+  }
+  for (int a = lane; a <= n; a += kWave) count[wv][a] = 0;  // (the wave's own)
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (mine[i] >= 0) atomicAdd(&count[wv][mine[i]], 1);
+  for (int t = t0 + KEEP * kWave + lane; t < t1; t += kWave) {
+    const int a = adapter[t];
+    atomicAdd(&count[wv][a >= 0 && a < n ? a : n], 1);
+  }
+  __syncthreads();
+  // thread a: adapter a's rows, and its rows' places wave by wave
+  int c[kPlanWaves], rows = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) c[w] = count[w][min(tid, n)];
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    rows += tid < n ? c[w] : 0;
+  }
+  const int nu = tid < n && units ? max(1, (rows + TS - 1) / TS) : 0;  // no rows: one unit of none
+  Four all;
+  const Four ex = block_scan({rows, (rows + kShrinkTile - 1) / kShrinkTile, nu, nu > 1 ? nu : 0}, s_w,
+                             &all);
+  const int rows_all = all.v[0], pos = tid < n ? ex.v[0] : rows_all;  // the rows without one: last
+  if (tid <= n) {
+    int at = pos;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      count[w][tid] = at;
+      at += c[w];
+    }
+    starts[tid] = pos;
+    tiles[tid] = tid < n ? ex.v[1] : all.v[1];
+    if (tid == n) {
+      starts[n + 1] = T;
+      tiles[n + 1] = all.v[1] + (T - rows_all + kShrinkTile - 1) / kShrinkTile;
+    }
+    if (units && tid < n) {
+      adapters[tid] = make_int2(ex.v[3], nu);
+      for (int i = 0; i < nu; ++i)
+        units[ex.v[2] + i] =
+            LoraUnit{tid, pos + i * TS, min(TS, rows - i * TS), nu > 1 ? ex.v[3] + i : -1};
+    }
+  }
+  if (n == kPlanWaves * kWave && tid == 0) {  // one bucket more than threads
+    int at = rows_all;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int q = count[w][n];
+      count[w][n] = at;
+      at += q;
+    }
+    starts[n] = rows_all;
+    starts[n + 1] = T;
+    tiles[n] = all.v[1];
+    tiles[n + 1] = all.v[1] + (T - rows_all + kShrinkTile - 1) / kShrinkTile;
+  }
+  if (tid == 0 && units) *n_units = all.v[2];
+  __syncthreads();
+  // 64 rows at a time: the lanes of a row's adapter by one ballot per bit of
+  // it; the first of them takes their places
+  auto place = [&](int a, int t) {
+    unsigned long long same = __ballot(a >= 0);
+    for (int bit = 0; (n >> bit) != 0; ++bit) {
+      const unsigned long long ones = __ballot((a >> bit) & 1);
+      same &= (a >> bit) & 1 ? ones : ~ones;
+    }
+    const int first = a >= 0 ? __builtin_ctzll(same) : lane;
+    int at = 0;
+    if (a >= 0 && lane == first) at = atomicAdd(&count[wv][a], (int)__popcll(same));
+    at = __shfl(at, first, kWave);
+    if (a >= 0) order[at + __popcll(same & ((1ull << lane) - 1))] = t;
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (t0 + i * kWave < t1) place(mine[i], t0 + i * kWave + lane);
+  for (int b = t0 + KEEP * kWave; b < t1; b += kWave) {
+    const int t = b + lane;
+    const int a = adapter[min(t, T - 1)];
+    place(t < t1 ? (a >= 0 && a < n ? a : n) : -1, t);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_lora_plan(const int32_t *adapter, int T, int n, const LoraPlan &p, bool units,
+                            char *ws, hipStream_t s) {
+  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(kPlanWaves * kWave), 0, s, adapter, T, n, p.TS,
+                     reinterpret_cast<int32_t *>(ws + p.order),
+                     reinterpret_cast<int32_t *>(ws + p.starts),
+                     reinterpret_cast<int32_t *>(ws + p.tiles),
+                     units ? reinterpret_cast<LoraUnit *>(ws + p.units) : nullptr,
+                     reinterpret_cast<int2 *>(ws + p.adapters),
+                     reinterpret_cast<int32_t *>(ws + p.n_units));
+  return hipGetLastError();
+}

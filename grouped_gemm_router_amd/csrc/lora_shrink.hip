@@ -8,11 +8,11 @@
 //   * few rows: one wave per (row, rank), whole rows read with 16-byte loads;
 //     the factors are read once per row that uses them, which is what a
 //     decode batch of different adapters has to read anyway;
-//   * many rows: 16 rows and 16 ranks per workgroup of eight waves.  Where
-//     the rows have few adapters (prompts), the waves cut K and the matrix
-//     cores multiply, one adapter after the other; partial sums meet in LDS
-//     in wave order.  Otherwise each wave takes a row and reads that row's
-//     own factors.
+//   * many rows, sorted by adapter (the plan): a workgroup takes up to 64 rows
+//     of one adapter, up to 64 ranks and a slice of K.  What bounds this is
+//     the rate at which a CU takes in operands (some 20 bytes a ns from beyond
+//     its L1, measured): 64 rows share each factor load, and K is cut so that
+//     every CU has its share; a second launch adds the slices in order.
 #include "lora_internal.h"
 
 namespace {
@@ -34,12 +34,13 @@ __device__ __forceinline__ float dot_piece(u32x4 a, u32x4 b, float acc) {
   return acc;
 }
 
-// grid (r / 4, T): four waves, one rank each
+// grid T r / 4: four waves, one (row, rank) each
 template <int ES>
 __global__ __launch_bounds__(256) void shrink_row_kernel(
     const char *__restrict__ x, const char *__restrict__ F, const float *__restrict__ scale,
     const int32_t *__restrict__ adapter, int K, int r, int n, float *__restrict__ v) {
-  const int t = blockIdx.y, j = blockIdx.x * 4 + threadIdx.x / kWave, lane = lane_id();
+  const int t = blockIdx.x / (r / 4), j = blockIdx.x % (r / 4) * 4 + threadIdx.x / kWave;
+  const int lane = lane_id();
   const int a = adapter[t];
   if (a < 0 || a >= n) {
     if (lane == 0) v[(size_t)t * r + j] = 0.f;
@@ -56,9 +57,8 @@ __global__ __launch_bounds__(256) void shrink_row_kernel(
     u32x4 xa[U], fa[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int p = p0 + u * kWave;
-      xa[u] = load_piece(xp, p, np);
-      fa[u] = load_piece(fp, p, np);
+      xa[u] = load_piece(xp, p0 + u * kWave, np);
+      fa[u] = load_piece(fp, p0 + u * kWave, np);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) acc[u] = dot_piece<ES>(xa[u], fa[u], acc[u]);
@@ -86,186 +86,209 @@ __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 acc) {
   }
 }
 
-// Sum of each of a lane's eight values over the wave: the result for value
-// lane & 7 (bit-reversed: value 4 (lane & 1) + 2 (lane >> 1 & 1) + (lane >> 2
-// & 1)).  Each of the first three steps halves the values that a lane still
-// holds, ten exchanges in all instead of 48; the order is fixed.
-__device__ __forceinline__ float sum8(float (&v)[8], int lane) {
+constexpr int kTileWaves = 4, kTileThreads = kTileWaves * kWave, kTileBlocks = kShrinkTile / 16;
+
+// One wave's share of a tile's sums over the pieces [p0, p_end): RB blocks of
+// 16 rows times NR blocks of 16 ranks, to red[row][rank].
+template <int ES, int RB, int NR>
+__device__ __forceinline__ void shrink_slice(const char *x, const char *F, const int *s_row, int K,
+                                             int r, int a, int j0, int p0, int p_end, int wv,
+                                             float (*red)[NR * 16 + 1]) {
+  const int lane = lane_id(), fr = lane & 15, fq = lane >> 4;
+  const u32x4 *xp[RB], *fp[NR];
 #pragma unroll
-  for (int h = 4, o = 1; h > 0; h >>= 1, o <<= 1) {
-    const bool up = lane & o;
+  for (int b = 0; b < RB; ++b)
+    xp[b] = reinterpret_cast<const u32x4 *>(x + (size_t)s_row[b * 16 + fr] * K * ES);
 #pragma unroll
-    for (int i = 0; i < h; ++i) {
-      const float send = up ? v[i] : v[i + h];
-      v[i] = (up ? v[i + h] : v[i]) + __shfl_xor(send, o, kWave);
+  for (int q = 0; q < NR; ++q)  // ranks behind r repeat the last one and are not stored
+    fp[q] = reinterpret_cast<const u32x4 *>(F + ((size_t)a * r + min(j0 + q * 16 + fr, r - 1)) * K * ES);
+  f32x4 acc[RB][NR];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int q = 0; q < NR; ++q) acc[b][q] = f32x4{};
+  // a wave takes U / 2 lines of every row at a time
+  constexpr int U = NR == 1 ? 4 : 2, CHUNK = U * kTileWaves * 4;
+  auto at = [&](int p, int u) {
+    return p + (2 * wv + (u & 1) + (u >> 1) * 2 * kTileWaves) * 4 + fq;
+  };
+  auto multiply = [&](const u32x4(&xa)[U][RB], const u32x4(&fa)[U][NR]) {
+    __builtin_amdgcn_sched_barrier(0);  // every load of the chunk is issued first
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int q = 0; q < NR; ++q) acc[b][q] = mma16<ES>(xa[u][b], fa[u][q], acc[b][q]);
+  };
+  for (; p0 + CHUNK <= p_end; p0 += CHUNK) {
+    u32x4 xa[U][RB], fa[U][NR];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) xa[u][b] = xp[b][at(p0, u)];
+#pragma unroll
+      for (int q = 0; q < NR; ++q) fa[u][q] = fp[q][at(p0, u)];
     }
+    multiply(xa, fa);
   }
-  float s = v[0];
+  if (p0 < p_end) {  // zeros behind the slice's end
+    u32x4 xa[U][RB], fa[U][NR];
 #pragma unroll
-  for (int o = 8; o < kWave; o <<= 1) s += __shfl_xor(s, o, kWave);
-  return s;
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) xa[u][b] = load_piece(xp[b], at(p0, u), p_end);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) fa[u][q] = load_piece(fp[q], at(p0, u), p_end);
+    }
+    multiply(xa, fa);
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int q = 0; q < NR; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[b * 16 + 4 * fq + i][q * 16 + fr] = acc[b][q][i];
 }
 
-constexpr int kShrinkWaves = 8;
-
-// Adapters among 16 rows up to which the tile takes them one after the other
-// on the matrix cores: a pass costs its latency and 32 rows of operands, the
-// other way 17 rows of operands per row.
-__device__ __forceinline__ bool few_adapters(int kinds, int row_bytes) {
-  return kinds <= 1 || kinds * 2048 <= row_bytes;
-}
-
-// one chunk's pieces of a wave: two neighbouring groups of 4 pieces (whole
-// 128-byte lines of every row) out of each 2 kShrinkWaves groups
-constexpr int kShrinkU = 4, kShrinkChunk = kShrinkU * kShrinkWaves * 4;
-
-struct ShrinkPieces {
-  u32x4 x[kShrinkU], f[kShrinkU];
-  static __device__ __forceinline__ int at(int u, int wv, int fq) {
-    return (2 * wv + (u & 1) + (u >> 1) * 2 * kShrinkWaves) * 4 + fq;
-  }
-  __device__ __forceinline__ void load(const u32x4 *xp, const u32x4 *fp, int p0, int wv, int fq) {
-#pragma unroll
-    for (int u = 0; u < kShrinkU; ++u) {
-      x[u] = xp[p0 + at(u, wv, fq)];
-      f[u] = fp[p0 + at(u, wv, fq)];
-    }
-  }
-  // the last chunk: zeros behind the row's np pieces
-  __device__ __forceinline__ void load_tail(const u32x4 *xp, const u32x4 *fp, int p0, int np, int wv,
-                                            int fq) {
-#pragma unroll
-    for (int u = 0; u < kShrinkU; ++u) {
-      x[u] = load_piece(xp, p0 + at(u, wv, fq), np);
-      f[u] = load_piece(fp, p0 + at(u, wv, fq), np);
-    }
-  }
-  template <int ES>
-  __device__ __forceinline__ f32x4 multiply(f32x4 acc) const {
-#pragma unroll
-    for (int u = 0; u < kShrinkU; ++u) acc = mma16<ES>(x[u], f[u], acc);
-    return acc;
-  }
+// A tile's adapter (n: none), first place in the order and number of rows.
+// tiles[a]: the adapters' first tiles (tiles[n]: of the rows without an
+// adapter, tiles[n + 1]: all); starts[a]: their first rows in the order.  The
+// adapter a with tiles[a] <= tile < tiles[a + 1] is found 64 probes at a time.
+// Must be called by whole waves.
+struct TileRows {
+  int a, first, rows;
 };
+__device__ __forceinline__ TileRows tile_rows(const int32_t *starts, const int32_t *tiles, int n,
+                                              int tile) {
+  int lo = 0, cnt = n + 1;
+  while (cnt > 0) {
+    const int step = (cnt + kWave - 1) / kWave;
+    const int i = lo + min(((int)lane_id() + 1) * step, cnt) - 1;
+    const unsigned long long behind = __ballot(tiles[i + 1] > tile);
+    if (behind == 0) {
+      lo += cnt;
+      break;
+    }
+    const int f = __builtin_ctzll(behind), hit = lo + min((f + 1) * step, cnt) - 1;
+    lo += f * step;
+    cnt = hit - lo;
+  }
+  const int first = starts[lo] + (tile - tiles[lo]) * kShrinkTile;
+  return {lo, first, min(starts[lo + 1] - first, kShrinkTile)};
+}
 
-// A workgroup per 16 rows and 16 ranks.  The rank blocks of a row tile run
-// next to each other on one XCD (workgroups are dealt to the 8 XCDs in turn),
-// so x comes from HBM once.
-template <int ES>
-__global__ __launch_bounds__(kShrinkWaves *kWave, 4) void shrink_tile_kernel(
+// grid (tiles times K slices, rank groups of 16 NR)
+template <int ES, int NR>
+__global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
     const char *__restrict__ x, const char *__restrict__ F, const float *__restrict__ scale,
-    const int32_t *__restrict__ adapter, int T, int K, int r, int n, float *__restrict__ v) {
-  __shared__ float red[kShrinkWaves][16][17];
-  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
-  const int fr = lane & 15, fq = lane >> 4;
-  const int blocks = (r + 15) / 16, i8 = blockIdx.x / 8;
-  const int t0 = ((i8 / blocks) * 8 + blockIdx.x % 8) * 16, j0 = (i8 % blocks) * 16;
-  if (t0 >= T) return;
-  const int np = K * ES / 16;
-  // the tile's adapters, the same answer in every wave (rows past T repeat
-  // the last one)
-  int a_mine = adapter[min(t0 + fr, T - 1)];
-  if (a_mine < 0 || a_mine >= n) a_mine = -1;
-  unsigned todo = (unsigned)__ballot(a_mine >= 0) & 0xffffu;
-  int kinds = 0;
-  for (unsigned left = todo; left; ++kinds)
-    left &= ~(unsigned)__ballot(a_mine == __builtin_amdgcn_readlane(a_mine, __builtin_ctz(left)));
-  if (few_adapters(kinds, K * ES)) {
-    if (tid < 256) {  // rows without an adapter
-      const int row = tid >> 4, j = tid & 15;
-      if (!((todo >> row) & 1) && t0 + row < T && j0 + j < r) v[(size_t)(t0 + row) * r + j0 + j] = 0.f;
-    }
-    const u32x4 *xp = reinterpret_cast<const u32x4 *>(x + (size_t)min(t0 + fr, T - 1) * K * ES);
-    while (todo) {
-      const int a = __builtin_amdgcn_readlane(a_mine, __builtin_ctz(todo));
-      const unsigned same = (unsigned)__ballot(a_mine == a) & 0xffffu;
-      todo &= ~same;
-      // ranks behind r repeat the last one and are not stored
-      const u32x4 *fp =
-          reinterpret_cast<const u32x4 *>(F + ((size_t)a * r + min(j0 + fr, r - 1)) * K * ES);
-      f32x4 acc = f32x4{};
-      int p0 = 0;
-      for (; p0 + kShrinkChunk <= np; p0 += kShrinkChunk) {
-        ShrinkPieces c;
-        c.load(xp, fp, p0, wv, fq);
-        __builtin_amdgcn_sched_barrier(0);  // every load is issued first
-        acc = c.multiply<ES>(acc);
+    const int32_t *__restrict__ order, const int32_t *__restrict__ starts,
+    const int32_t *__restrict__ tiles, int max_tiles, int slices, int K, int r, int n,
+    float *__restrict__ part, float *__restrict__ v) {
+  constexpr int RP = NR * 16;
+  __shared__ float red[kTileWaves][kShrinkTile][RP + 1];
+  __shared__ int s_row[kShrinkTile];
+  const int tid = threadIdx.x, wv = tid / kWave;
+  const int tile = blockIdx.x / slices, ks = blockIdx.x % slices, j0 = blockIdx.y * RP;
+  if (tile >= tiles[n + 1]) return;
+  const TileRows tr = tile_rows(starts, tiles, n, tile);
+  const int a = tr.a, rows = tr.rows;
+  if (a == n) {  // rows without an adapter
+    if (ks == 0)
+      for (int i = tid; i < rows * RP; i += kTileThreads) {
+        const int j = j0 + i % RP;
+        if (j < r) v[(size_t)order[tr.first + i / RP] * r + j] = 0.f;
       }
-      if (p0 < np) {
-        ShrinkPieces c;
-        c.load_tail(xp, fp, p0, np, wv, fq);
-        __builtin_amdgcn_sched_barrier(0);
-        acc = c.multiply<ES>(acc);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[wv][4 * fq + i][fr] = acc[i];
-      __syncthreads();
-      if (tid < 256) {
-        const int row = tid >> 4, j = tid & 15;
-        float sum = red[0][row][j];
-#pragma unroll
-        for (int w = 1; w < kShrinkWaves; ++w) sum += red[w][row][j];
-        if (((same >> row) & 1) && t0 + row < T && j0 + j < r)
-          v[(size_t)(t0 + row) * r + j0 + j] = scale[a] * sum;
-      }
-      __syncthreads();
-    }
     return;
   }
-  // rows of many adapters: a row per wave at a time, eight ranks of it
-  for (int t = t0 + wv; t < min(t0 + 16, T); t += kShrinkWaves) {
-    const int a = adapter[t];
-    const bool none = a < 0 || a >= n;
-    const u32x4 *xp = reinterpret_cast<const u32x4 *>(x + (size_t)t * K * ES);
-    for (int j = j0; j < min(j0 + 16, r); j += 8) {
-      float acc[8];
+  if (tid < kShrinkTile) s_row[tid] = order[tr.first + min(tid, rows - 1)];
+  __syncthreads();
+  const int np = K * ES / 16;
+  // this slice's pieces: whole lines of 8, the same number for every slice
+  const int per = ((np + 7) / 8 + slices - 1) / slices * 8;
+  const int p_end = min(np, (ks + 1) * per);
+  const int live = (rows + 15) / 16;  // row blocks
+  const int p0 = ks * per;
+  if (live <= 1) shrink_slice<ES, 1, NR>(x, F, s_row, K, r, a, j0, p0, p_end, wv, red[wv]);
+  else if (live <= 2) shrink_slice<ES, 2, NR>(x, F, s_row, K, r, a, j0, p0, p_end, wv, red[wv]);
+  else shrink_slice<ES, kTileBlocks, NR>(x, F, s_row, K, r, a, j0, p0, p_end, wv, red[wv]);
+  __syncthreads();
+  float *mine = part + (((size_t)blockIdx.y * max_tiles + tile) * slices + ks) * kShrinkTile * RP;
+  for (int i = tid; i < live * 16 * RP; i += kTileThreads) {
+    const int row = i / RP, j = i % RP;
+    float sum = red[0][row][j];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-      if (!none) {
-        const u32x4 *fp = reinterpret_cast<const u32x4 *>(F + ((size_t)a * r + j) * K * ES);
-        constexpr int U = 1;
-        for (int p0 = lane; p0 < np; p0 += U * kWave) {
-          u32x4 xa[U], fa[U][8];
+    for (int w = 1; w < kTileWaves; ++w) sum += red[w][row][j];
+    if (slices > 1)
+      mine[i] = sum;
+    else if (row < rows && j0 + j < r)
+      v[(size_t)s_row[row] * r + j0 + j] = scale[a] * sum;
+  }
+}
+
+// The tiles' slices added in slice order.  A launch of its own: a flag between
+// workgroups of the same launch needs their XCDs' L2 written back, which took
+// five times as long as the products.  grid (4 parts of a tile's rows times
+// tiles, rank groups)
+__global__ __launch_bounds__(256) void shrink_sum_kernel(
+    const float *__restrict__ part, const float *__restrict__ scale,
+    const int32_t *__restrict__ order, const int32_t *__restrict__ starts,
+    const int32_t *__restrict__ tiles, int max_tiles, int slices, int RP, int r, int n,
+    float *__restrict__ v) {
+  const int tile = blockIdx.x / 4, j0 = blockIdx.y * RP;
+  if (tile >= tiles[n + 1]) return;
+  const TileRows tr = tile_rows(starts, tiles, n, tile);
+  if (tr.a == n) return;
+  const float *all = part + ((size_t)blockIdx.y * max_tiles + tile) * slices * kShrinkTile * RP;
+  const int r0 = (blockIdx.x % 4) * (kShrinkTile / 4);
+  for (int i = threadIdx.x; i < kShrinkTile / 4 * RP; i += 256) {
+    const int row = r0 + i / RP, j = i % RP;
+    if (row >= tr.rows || j0 + j >= r) continue;
+    float p[kShrinkSlices];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            xa[u] = load_piece(xp, p0 + u * kWave, np);
+    for (int k = 0; k < kShrinkSlices; ++k)
+      p[k] = all[((size_t)min(k, slices - 1) * kShrinkTile + row) * RP + j];
+    float sum = p[0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              fa[u][i] = load_piece(fp + (size_t)i * np, p0 + u * kWave, np);
-          }
-          __builtin_amdgcn_sched_barrier(0);  // every load is issued first
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = dot_piece<ES>(xa[u], fa[u][i], acc[i]);
-        }
-      }
-      const float s = sum8(acc, lane);
-      const int which = 4 * (lane & 1) + (lane & 2) + ((lane >> 2) & 1);
-      if (lane < 8) v[(size_t)t * r + j + which] = none ? 0.f : scale[a] * s;
-    }
+    for (int k = 1; k < kShrinkSlices; ++k) sum += k < slices ? p[k] : 0.f;
+    v[(size_t)order[tr.first + row] * r + j0 + j] = scale[tr.a] * sum;
   }
 }
 
 template <int ES>
-void launch_t(const void *x, const void *F, const float *scale, const int32_t *adapter, int T, int K,
-              int r, int n, float *v, hipStream_t s) {
+void launch_t(const void *x, const void *F, const float *scale, const int32_t *adapter,
+              const LoraPlan *p, char *ws, int T, int K, int r, int n, float *v, hipStream_t s) {
   const char *xb = static_cast<const char *>(x), *fb = static_cast<const char *>(F);
-  if (T <= kShrinkRowMax) {
-    hipLaunchKernelGGL((shrink_row_kernel<ES>), dim3(r / 4, T), dim3(256), 0, s, xb, fb, scale,
-                       adapter, K, r, n, v);
+  if (!p) {
+    hipLaunchKernelGGL((shrink_row_kernel<ES>), dim3((unsigned)T * (r / 4)), dim3(256), 0, s, xb, fb,
+                       scale, adapter, K, r, n, v);
     return;
   }
-  hipLaunchKernelGGL((shrink_tile_kernel<ES>), dim3(((T + 15) / 16 + 7) / 8 * 8 * ((r + 15) / 16)),
-                     dim3(kShrinkWaves * kWave), 0, s, xb, fb, scale, adapter, T, K, r, n, v);
+  const int NR = r <= 16 ? 1 : r <= 32 ? 2 : 4, groups = (r + 16 * NR - 1) / (16 * NR);
+  const int slices = lora_shrink_slices(T, K * ES, r);
+  const dim3 grid((unsigned)p->max_tiles * slices, groups), block(kTileThreads);
+  const int32_t *order = reinterpret_cast<const int32_t *>(ws + p->order);
+  const int32_t *starts = reinterpret_cast<const int32_t *>(ws + p->starts);
+  const int32_t *tiles = reinterpret_cast<const int32_t *>(ws + p->tiles);
+  float *part = reinterpret_cast<float *>(ws + p->part);
+#define MOE_SHRINK(NR)                                                                          \
+  hipLaunchKernelGGL((shrink_tile_kernel<ES, NR>), grid, block, 0, s, xb, fb, scale, order, starts, \
+                     tiles, p->max_tiles, slices, K, r, n, part, v)
+  if (NR == 1) MOE_SHRINK(1);
+  else if (NR == 2) MOE_SHRINK(2);
+  else MOE_SHRINK(4);
+#undef MOE_SHRINK
+  if (slices > 1)
+    hipLaunchKernelGGL(shrink_sum_kernel, dim3((unsigned)p->max_tiles * 4, groups), dim3(256), 0, s,
+                       part, scale, order, starts, tiles, p->max_tiles, slices, 16 * NR, r, n, v);
 }
 
 }  // namespace
 
 hipError_t launch_lora_shrink(const void *x, const void *F, int dt, const float *scale,
-                              const int32_t *adapter, int T, int K, int r, int n, float *v,
-                              hipStream_t s) {
-  if (dt == MOE_BF16) launch_t<2>(x, F, scale, adapter, T, K, r, n, v, s);
-  else launch_t<4>(x, F, scale, adapter, T, K, r, n, v, s);
+                              const int32_t *adapter, const LoraPlan *p, char *ws, int T, int K,
+                              int r, int n, float *v, hipStream_t s) {
+  if (dt == MOE_BF16) launch_t<2>(x, F, scale, adapter, p, ws, T, K, r, n, v, s);
+  else launch_t<4>(x, F, scale, adapter, p, ws, T, K, r, n, v, s);
   return hipGetLastError();
 }

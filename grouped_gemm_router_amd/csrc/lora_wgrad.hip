@@ -2,145 +2,40 @@
 //   dA[a][j] = sum over its rows t of u[t][j] x[t],
 //   dB[a][j] = sum over its rows t of v[t][j] dy[t].
 //
-// The rows of an adapter may lie anywhere in the batch, so one small launch
-// sorts the rows by adapter (stably, so every sum has a fixed order) and cuts
-// each adapter's rows into units of at most TS.  The second launch is the
-// product: a workgroup takes a unit, 128 columns and 16 or 32 ranks, and its
+// The rows are read in the plan's order, adapter by adapter, and each
+// adapter's rows are cut into units of at most TS.  A workgroup takes a unit, 128 columns and 16 or 32 ranks, and its
 // four waves take 32 rows in turn.  The sum runs over rows, so a lane loads
 // 16 bytes (8 columns) of 8 rows and turns that 8 x 8 block in registers into
 // eight matrix-core fragments; x and dy are read once, in whole lines, which
 // is what bounds this (2 r flops per 2 bytes).  u and v are fp32 and enter as
 // three bf16 terms each, so no bit of them is lost.  A unit that is all of
 // its adapter writes the gradient itself; the slices of a longer one go to
-// the workspace and a third launch adds them in order.
+// the workspace and a second launch adds them in order.
 #include "lora_internal.h"
 
 namespace {
 
 using namespace moe;
 
-constexpr int kPlanWaves = 16;
 constexpr int kColTile = 128;
 
-// rows per unit: at most 64 slices to add; batches of up to kUnitRows rows
-// are never sliced and need no third launch
-constexpr int kUnitRows = 1024;
-int unit_rows(int T) {
-  const int by = ((T + 31) / 32 + 31) / 32 * 32;
-  return by > kUnitRows ? by : kUnitRows;
-}
-
-struct Unit {
-  int adapter, pos, count, slot;  // slot < 0: the adapter's only unit
-};
-
-struct Ws {
-  size_t order, units, adapters, n_units, part, bytes;
-  int TS, max_units;
-};
-
-Ws layout(int T, int N, int K, int r, int n) {
-  Ws w;
-  w.TS = unit_rows(T);
-  w.max_units = T / w.TS + n;  // (an adapter without rows has one of no rows)
-  // an adapter of c > TS rows has fewer than 2 c / TS units
-  const size_t slots = T <= w.TS ? 0 : 2 * (size_t)T / w.TS + 1;
-  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  w.order = 0;
-  w.units = up((size_t)T * 4);
-  w.adapters = w.units + up((size_t)w.max_units * sizeof(Unit));
-  w.n_units = w.adapters + up((size_t)n * 8);
-  w.part = w.n_units + 256;
-  w.bytes = w.part + slots * r * ((size_t)K + N) * 4;
-  return w;
-}
-
-// exclusive scan over the workgroup's 1024 threads; *total: the sum
-__device__ __forceinline__ int block_scan(int v, int *s_w, int *total) {
-  const int wv = threadIdx.x / kWave;
-  int sum;
-  const int ex = wave_exclusive_scan(v, &sum);
-  if (lane_id() == 0) s_w[wv] = sum;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kPlanWaves; ++w) {
-    if (w < wv) before += s_w[w];
-    all += s_w[w];
-  }
-  __syncthreads();
-  *total = all;
-  return ex + before;
-}
-
-// One workgroup.  Wave w takes the w-th sixteenth of the rows; count[w][a]
-// becomes the place of its next row of adapter a.
-__global__ __launch_bounds__(kPlanWaves *kWave) void wgrad_plan_kernel(
-    const int32_t *__restrict__ adapter, int T, int n, int TS, int32_t *__restrict__ order,
-    Unit *__restrict__ units, int2 *__restrict__ adapters, int32_t *__restrict__ n_units) {
-  __shared__ int count[kPlanWaves][MOE_LORA_MAX_ADAPTERS];
-  __shared__ int s_w[kPlanWaves];
-  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
-  for (int i = tid; i < kPlanWaves * n; i += kPlanWaves * kWave) count[i / n][i % n] = 0;
-  __syncthreads();
-  const int chunk = ((T + kPlanWaves - 1) / kPlanWaves + kWave - 1) / kWave * kWave;
-  const long long c0 = (long long)wv * chunk;
-  const int t0 = (int)min(c0, (long long)T), t1 = (int)min(c0 + chunk, (long long)T);
-  for (int t = t0 + lane; t < t1; t += kWave) {
-    const int a = adapter[t];
-    if (a >= 0 && a < n) atomicAdd(&count[wv][a], 1);
-  }
-  __syncthreads();
-  int mine = 0;
-  if (tid < n)
-    for (int w = 0; w < kPlanWaves; ++w) mine += count[w][tid];
-  const int nu = tid < n ? max(1, (mine + TS - 1) / TS) : 0;
-  int rows_all, units_all, slots_all;
-  const int pos = block_scan(mine, s_w, &rows_all);
-  const int u0 = block_scan(nu, s_w, &units_all);
-  const int slot0 = block_scan(nu > 1 ? nu : 0, s_w, &slots_all);
-  if (tid < n) {
-    int at = pos;
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = count[w][tid];
-      count[w][tid] = at;
-      at += c;
-    }
-    adapters[tid] = make_int2(slot0, nu);
-    for (int i = 0; i < nu; ++i)
-      units[u0 + i] = Unit{tid, pos + i * TS, min(TS, mine - i * TS), nu > 1 ? slot0 + i : -1};
-  }
-  if (tid == 0) *n_units = units_all;
-  __syncthreads();
-  // this wave's row of count only, lane to lane: volatile, so that every turn
-  // reads what the turn before stored
-  volatile int *next = count[wv];
-  for (int b = t0; b < t1; b += kWave) {
-    const int t = b + lane;
-    int a = t < t1 ? adapter[t] : -1;
-    if (a < 0 || a >= n) a = -1;
-    unsigned long long todo = __ballot(a >= 0);
-    while (todo) {  // one turn per adapter among these 64 rows
-      const int first = __builtin_ctzll(todo);
-      const int who = __builtin_amdgcn_readlane(a, first);
-      const unsigned long long same = __ballot(a == who);
-      const int at = next[who];
-      if (a == who) order[at + __popcll(same & ((1ull << lane) - 1))] = t;
-      if (lane == first) next[who] = at + __popcll(same);
-      todo &= ~same;
-    }
-  }
+// the slices behind the plan: an adapter of c > TS rows has fewer than
+// 2 c / TS units
+size_t slices_bytes(const LoraPlan &p, int T, int N, int K, int r) {
+  const size_t slots = T <= p.TS ? 0 : 2 * (size_t)T / p.TS + 1;
+  return slots * r * ((size_t)K + N) * 4;
 }
 
 // grid (units, column tiles of x then of dy, rank groups of 16 NR)
 template <int ES, int NR>
 __global__ __launch_bounds__(256) void wgrad_kernel(
     const char *__restrict__ x, const char *__restrict__ dy, const float *__restrict__ u,
-    const float *__restrict__ v, const int32_t *__restrict__ order, const Unit *__restrict__ units,
+    const float *__restrict__ v, const int32_t *__restrict__ order, const LoraUnit *__restrict__ units,
     const int32_t *__restrict__ n_units, int N, int K, int r, float *__restrict__ dA,
     float *__restrict__ dB, float *__restrict__ part) {
   __shared__ float red[4][16][kColTile + 4];
   if ((int)blockIdx.x >= *n_units) return;
-  const Unit un = units[blockIdx.x];
+  const LoraUnit un = units[blockIdx.x];
   const int ka = (K + kColTile - 1) / kColTile;
   const bool is_a = (int)blockIdx.y < ka;
   const int C = is_a ? K : N, c0 = (is_a ? blockIdx.y : blockIdx.y - ka) * kColTile;
@@ -258,41 +153,40 @@ __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const int2 *__restric
 }
 
 template <int ES>
-void launch_t(const void *dy, const void *x, const float *u, const float *v, const Ws &w, char *ws,
-              int N, int K, int r, float *dA, float *dB, hipStream_t s) {
+void launch_t(const void *dy, const void *x, const float *u, const float *v, const LoraPlan &p,
+              char *ws, int N, int K, int r, float *dA, float *dB, hipStream_t s) {
   const int cols = (K + kColTile - 1) / kColTile + (N + kColTile - 1) / kColTile;
-  const int32_t *order = reinterpret_cast<const int32_t *>(ws + w.order);
-  const Unit *units = reinterpret_cast<const Unit *>(ws + w.units);
-  const int32_t *nu = reinterpret_cast<const int32_t *>(ws + w.n_units);
-  float *part = reinterpret_cast<float *>(ws + w.part);
+  const int32_t *order = reinterpret_cast<const int32_t *>(ws + p.order);
+  const LoraUnit *units = reinterpret_cast<const LoraUnit *>(ws + p.units);
+  const int32_t *nu = reinterpret_cast<const int32_t *>(ws + p.n_units);
+  float *part = reinterpret_cast<float *>(ws + p.bytes);
   const char *xb = static_cast<const char *>(x), *db = static_cast<const char *>(dy);
   if (r <= 16)
-    hipLaunchKernelGGL((wgrad_kernel<ES, 1>), dim3(w.max_units, cols, 1), dim3(256), 0, s, xb, db, u,
+    hipLaunchKernelGGL((wgrad_kernel<ES, 1>), dim3(p.max_units, cols, 1), dim3(256), 0, s, xb, db, u,
                        v, order, units, nu, N, K, r, dA, dB, part);
   else
-    hipLaunchKernelGGL((wgrad_kernel<ES, 2>), dim3(w.max_units, cols, (r + 31) / 32), dim3(256), 0, s,
+    hipLaunchKernelGGL((wgrad_kernel<ES, 2>), dim3(p.max_units, cols, (r + 31) / 32), dim3(256), 0, s,
                        xb, db, u, v, order, units, nu, N, K, r, dA, dB, part);
 }
 
 }  // namespace
 
-size_t lora_wgrad_ws_bytes(int T, int N, int K, int r, int n) { return layout(T, N, K, r, n).bytes; }
+size_t lora_wgrad_ws_bytes(int T, int N, int K, int r, int n, int es) {
+  const LoraPlan p = lora_plan(T, N, K, r, n, es, true);
+  return p.bytes + slices_bytes(p, T, N, K, r);
+}
 
 hipError_t launch_lora_wgrad(const void *dy, const void *x, int dt, const float *u, const float *v,
-                             const int32_t *adapter, int T, int N, int K, int r, int n, float *dA,
-                             float *dB, void *ws, hipStream_t s) {
-  const Ws w = layout(T, N, K, r, n);
+                             int T, int N, int K, int r, int n, float *dA, float *dB, void *ws,
+                             hipStream_t s) {
+  const LoraPlan p = lora_plan(T, N, K, r, n, dt == MOE_BF16 ? 2 : 4, true);
   char *b = static_cast<char *>(ws);
-  hipLaunchKernelGGL(wgrad_plan_kernel, dim3(1), dim3(kPlanWaves * kWave), 0, s, adapter, T, n, w.TS,
-                     reinterpret_cast<int32_t *>(b + w.order), reinterpret_cast<Unit *>(b + w.units),
-                     reinterpret_cast<int2 *>(b + w.adapters),
-                     reinterpret_cast<int32_t *>(b + w.n_units));
-  if (dt == MOE_BF16) launch_t<2>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
-  else launch_t<4>(dy, x, u, v, w, b, N, K, r, dA, dB, s);
-  if (T <= w.TS) return hipGetLastError();
+  if (dt == MOE_BF16) launch_t<2>(dy, x, u, v, p, b, N, K, r, dA, dB, s);
+  else launch_t<4>(dy, x, u, v, p, b, N, K, r, dA, dB, s);
+  if (T <= p.TS) return hipGetLastError();
   const long long pieces = (long long)r * ((K + N) / 4);
   hipLaunchKernelGGL(wgrad_reduce_kernel, dim3((unsigned)((pieces + 255) / 256), n), dim3(256), 0, s,
-                     reinterpret_cast<const int2 *>(b + w.adapters),
-                     reinterpret_cast<const float *>(b + w.part), N, K, r, dA, dB);
+                     reinterpret_cast<const int2 *>(b + p.adapters),
+                     reinterpret_cast<const float *>(b + p.bytes), N, K, r, dA, dB);
   return hipGetLastError();
 }

@@ -358,6 +358,8 @@ moe_status_t moe_route_backward(const float *logits, const int32_t *topk_idx,
 
 namespace {
 
+int size_of(moe_dtype_t dt) { return dt == MOE_BF16 ? 2 : 4; }
+
 // the sizes of both lora entries
 moe_status_t lora_sizes(int T, int N, int K, int r, int n, moe_dtype_t dt) {
   if (T < 0 || N < 1 || K < 1 || r < 1 || n < 1) return MOE_ERR_INVALID;
@@ -375,14 +377,14 @@ moe_status_t lora_sizes(int T, int N, int K, int r, int n, moe_dtype_t dt) {
 bool pitch_ok(int *ld, int row, moe_dtype_t dt, const void *w) {
   if (!w) return *ld == 0;
   if (*ld == 0) *ld = row;
-  return *ld >= row && (long long)*ld * (dt == MOE_BF16 ? 2 : 4) % 16 == 0 && aligned16(w);
+  return *ld >= row && (long long)*ld * size_of(dt) % 16 == 0 && aligned16(w);
 }
 
 }  // namespace
 
 size_t moe_lora_linear_workspace_size(int T, int N, int K, int r, int n, moe_dtype_t dt) {
-  (void)T, (void)N, (void)K, (void)r, (void)n, (void)dt;
-  return 0;
+  if (lora_sizes(T, N, K, r, n, dt) != MOE_OK || !lora_sorts(T, N, K, r, size_of(dt))) return 0;
+  return lora_plan(T, N, K, r, n, size_of(dt), false).bytes;
 }
 
 moe_status_t moe_lora_linear(const void *x, const void *W, int ldw, const void *A,
@@ -398,17 +400,30 @@ moe_status_t moe_lora_linear(const void *x, const void *W, int ldw, const void *
       !aligned4(scale) || !aligned4(adapter) || !pitch_ok(&ldw, K, dt, W))
     return MOE_ERR_INVALID;
   if (ws == nullptr && ws_bytes != 0) return MOE_ERR_INVALID;
-  if (ws_bytes < moe_lora_linear_workspace_size(T, N, K, r, n, dt)) return MOE_ERR_WORKSPACE;
+  const size_t need = moe_lora_linear_workspace_size(T, N, K, r, n, dt);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return MOE_ERR_INVALID;
   const hipStream_t s = as_stream(stream);
-  const hipError_t e = launch_lora_shrink(x, A, dt, scale, adapter, T, K, r, n, v, s);
-  if (e != hipSuccess) return launched(e);
-  return launched(launch_lora_expand(x, W, ldw, B, dt, v, adapter, T, N, K, r, n, y, y_dt,
-                                     current_device_cus(), s));
+  hipError_t e = hipSuccess;
+  LoraPlan p;
+  char *const b = static_cast<char *>(ws);
+  const bool sorted = need > 0;
+  if (sorted) {
+    p = lora_plan(T, N, K, r, n, size_of(dt), false);
+    e = launch_lora_plan(adapter, T, n, p, false, b, s);
+  }
+  if (e == hipSuccess)
+    e = launch_lora_shrink(x, A, dt, scale, adapter, sorted ? &p : nullptr, b, T, K, r, n, v, s);
+  if (e == hipSuccess)
+    e = launch_lora_expand(x, W, ldw, B, dt, v, adapter,
+                           sorted ? reinterpret_cast<const int32_t *>(b + p.order) : nullptr, T, N, K,
+                           r, n, y, y_dt, current_device_cus(), s);
+  return launched(e);
 }
 
 size_t moe_lora_backward_workspace_size(int T, int N, int K, int r, int n, moe_dtype_t dt) {
   if (lora_sizes(T, N, K, r, n, dt) != MOE_OK || N % 8 != 0) return 0;
-  return lora_wgrad_ws_bytes(T, N, K, r, n);
+  return lora_wgrad_ws_bytes(T, N, K, r, n, size_of(dt));
 }
 
 moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void *W_t, int ldw,
@@ -421,29 +436,30 @@ moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void 
   if (sizes != MOE_OK) return sizes;
   if (N % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if ((dA == nullptr) != (dB == nullptr) || (!dx && !dA)) return MOE_ERR_INVALID;
-  if (dA) {
-    if (!aligned16(dA) || !aligned16(dB)) return MOE_ERR_INVALID;
-    if (ws_bytes < lora_wgrad_ws_bytes(T, N, K, r, n)) return MOE_ERR_WORKSPACE;
-    if (!aligned16(ws)) return MOE_ERR_INVALID;
+  if (dA && (!aligned16(dA) || !aligned16(dB))) return MOE_ERR_INVALID;
+  if (T > 0) {
+    if (!aligned16(dy) || !aligned16(A) || !aligned16(B) || !aligned16(u) || !aligned4(scale) ||
+        !aligned4(adapter))
+      return MOE_ERR_INVALID;
+    if (dx ? !aligned16(dx) || !pitch_ok(&ldw, N, dt, W_t) : W_t != nullptr || ldw != 0)
+      return MOE_ERR_INVALID;
+    if (dA && (!aligned16(x) || !aligned16(v))) return MOE_ERR_INVALID;
   }
-  if (T == 0) {  // no row of any adapter: zeros
-    if (!dA) return MOE_OK;
-    return launched(launch_lora_wgrad(dy, x, dt, u, v, adapter, T, N, K, r, n, dA, dB, ws,
-                                      as_stream(stream)));
-  }
-  if (!aligned16(dy) || !aligned16(A) || !aligned16(B) || !aligned16(u) || !aligned4(scale) ||
-      !aligned4(adapter))
-    return MOE_ERR_INVALID;
-  if (dx ? !aligned16(dx) || !pitch_ok(&ldw, N, dt, W_t) : W_t != nullptr || ldw != 0)
-    return MOE_ERR_INVALID;
-  if (dA && (!aligned16(x) || !aligned16(v))) return MOE_ERR_INVALID;
+  if (ws_bytes < lora_wgrad_ws_bytes(T, N, K, r, n, size_of(dt))) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_INVALID;
+  if (T == 0 && !dA) return MOE_OK;
   const hipStream_t s = as_stream(stream);
-  hipError_t e = launch_lora_shrink(dy, B, dt, scale, adapter, T, N, r, n, u, s);
-  if (e == hipSuccess && dx)
-    e = launch_lora_expand(dy, W_t, ldw, A, dt, u, adapter, T, K, N, r, n, dx, dt,
+  const LoraPlan p = lora_plan(T, N, K, r, n, size_of(dt), true);
+  char *const b = static_cast<char *>(ws);
+  const int32_t *order = reinterpret_cast<const int32_t *>(b + p.order);
+  hipError_t e = launch_lora_plan(adapter, T, n, p, true, b, s);
+  if (e == hipSuccess && T > 0)
+    e = launch_lora_shrink(dy, B, dt, scale, adapter, &p, b, T, N, r, n, u, s);
+  if (e == hipSuccess && T > 0 && dx)
+    e = launch_lora_expand(dy, W_t, ldw, A, dt, u, adapter, order, T, K, N, r, n, dx, dt,
                            current_device_cus(), s);
-  if (e == hipSuccess && dA)
-    e = launch_lora_wgrad(dy, x, dt, u, v, adapter, T, N, K, r, n, dA, dB, ws, s);
+  if (e == hipSuccess && dA)  // (T == 0: no row of any adapter, zeros)
+    e = launch_lora_wgrad(dy, x, dt, u, v, T, N, K, r, n, dA, dB, ws, s);
   return launched(e);
 }
 

@@ -79,6 +79,10 @@ def test_lora_linear_validation(lib):
                 dict(dt=F32), dict(T=(1 << 24) + 1), dict(N=(1 << 20) + 1),
                 dict(T=1 << 24, N=1 << 13)):
         assert f(**bad) == UNSUPPORTED, bad
+    big = dict(T=1000, N=4096, K=4096)
+    need = lib.moe_lora_linear_workspace_size(1000, 4096, 4096, 8, 2, BF16)
+    assert need > 0 and f(**big, ws=P, wsb=need - 1) == WORKSPACE
+    assert f(**big, ws=MIS, wsb=need) == INVALID
 
 
 def test_lora_backward_validation(lib):
@@ -86,7 +90,7 @@ def test_lora_backward_validation(lib):
           dx=P, dA=P, dB=P, ws=P, wsb=BIG):
         return lib.moe_lora_linear_backward(dy, x, W, ldw, A, B, dt, sc, ad, v, T, N, K, r, n, u, dx,
                                             dA, dB, ws, wsb, NUL)
-    assert f(T=0, dA=NUL, dB=NUL, ws=NUL, wsb=0, x=NUL, v=NUL) == OK
+    assert f(T=0, dA=NUL, dB=NUL, x=NUL, v=NUL) == OK
     for bad in (dict(dA=NUL), dict(dB=NUL), dict(dx=NUL), dict(dx=NUL, W=NUL, dA=NUL, dB=NUL),
                 dict(dy=MIS), dict(x=NUL), dict(v=NUL), dict(u=NUL), dict(dx=MIS), dict(ws=NUL),
                 dict(ws=MIS), dict(ldw=56), dict(W=NUL, ldw=64), dict(r=-8)):
