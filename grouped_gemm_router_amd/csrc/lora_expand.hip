@@ -337,36 +337,50 @@ __device__ __forceinline__ void finish_rows(StageOf stage_of, int first, int str
 }
 
 // ---------------------------------------------------------------------------
-// fp32: tiles of 64 x 64 on 4 waves of 32 x 32, operands through LDS 128
-// bytes of a row at a time: the next step's pieces are loaded into registers
-// while this step is multiplied.  Pieces past K read as zero; rows past T and
-// columns past N repeat the last one and are not stored.  Every row's
-// low-rank part runs on the vector ALUs in fp32.
+// fp32: every row's low-rank part runs on the vector ALUs in fp32, and no sum
+// over K is longer than K / 2, or K / 8, terms before it meets the others.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void expand_f32_kernel(
+
+// acc += a b over the lane's 16-byte pieces: component c of the two halves'
+// pieces is k = 8 i + 4 (lane / 32) + c
+__device__ __forceinline__ f32x16 mma_f32(u32x4 a, u32x4 b, f32x16 acc) {
+  const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[c], fb[c], acc, 0, 0, 0);
+  return acc;
+}
+
+// Tiles of 64 x 64 on two groups of 4 waves of 32 x 32, operands through LDS
+// 256 bytes of a row at a time, 128 of them for each group: the next step's
+// pieces are loaded into registers while this step is multiplied.  Pieces past
+// K read as zero; rows past T and columns past N repeat the last one and are
+// not stored.
+constexpr int kF32Threads = 512;
+
+__global__ __launch_bounds__(kF32Threads) void expand_f32_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
     const float *__restrict__ v, const int32_t *__restrict__ adapter,
     const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
     int NT) {
-  constexpr int BM = 64, BNF = 64, SP = BNF + 4, NLD = (BM + BNF) * 8 / 256;
-  __shared__ u32x4 ring[2][(BM + BNF) * 8];
+  constexpr int BM = 64, BNF = 64, SP = BNF + 4, ROWS = BM + BNF, NLD = 2 * ROWS * 8 / kF32Threads;
+  __shared__ u32x4 ring[2][2][ROWS * 8];  // step parity, group
   __shared__ int s_row[BM], s_ad[BM];
   __shared__ int s_hom[BM / 32];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
   const int m0 = at.mt * BM, n0 = at.nt * BNF;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
-  const int wm = wv / 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
+  const int grp = wv / 4, wm = wv / 2 % 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
   if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   if (tid < BM / 32) s_hom[tid] = 0;
   f32x16 acc = f32x16{};
   __syncthreads();
   if (W) {
-    const int KP = K / 4, KT = (KP + 7) / 8;
+    const int KP = K / 4, KT = (KP + 15) / 16;
     const u32x4 *src[NLD];
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
-      const int row = (tid + 256 * i) >> 3;
+      const int row = (tid + kF32Threads * i) >> 4;  // 16 pieces a row and step
       src[i] = row < BM
                    ? reinterpret_cast<const u32x4 *>(x + (size_t)s_row[row] * K * 4)
                    : reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + row - BM, N - 1) * ldw * 4);
@@ -374,16 +388,13 @@ __global__ __launch_bounds__(256) void expand_f32_kernel(
     u32x4 reg[NLD];
     auto fetch = [&](int kt) {
 #pragma unroll
-      for (int i = 0; i < NLD; ++i) {
-        const int p = kt * 8 + (tid & 7);
-        reg[i] = load_piece(src[i], p, KP);
-      }
+      for (int i = 0; i < NLD; ++i) reg[i] = load_piece(src[i], kt * 16 + (tid & 15), KP);
     };
     auto put = [&](int b) {
 #pragma unroll
       for (int i = 0; i < NLD; ++i) {
-        const int row = (tid + 256 * i) >> 3;
-        ring[b][row * 8 + swzb(row, tid & 7)] = reg[i];
+        const int row = (tid + kF32Threads * i) >> 4;
+        ring[b][(tid >> 3) & 1][row * 8 + swzb(row, tid & 7)] = reg[i];
       }
     };
     fetch(0);
@@ -391,27 +402,95 @@ __global__ __launch_bounds__(256) void expand_f32_kernel(
     __syncthreads();
     for (int kt = 0; kt < KT; ++kt) {
       if (kt + 1 < KT) fetch(kt + 1);
+      const u32x4 *l = ring[kt & 1][grp];
+      const int ra = wm * 32 + fr, rb = BM + wn * 32 + fr;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int ra = wm * 32 + fr, rb = BM + wn * 32 + fr;
-        const f32x4 a = __builtin_bit_cast(f32x4, ring[kt & 1][ra * 8 + swzb(ra, 2 * ks + fh)]);
-        const f32x4 b = __builtin_bit_cast(f32x4, ring[kt & 1][rb * 8 + swzb(rb, 2 * ks + fh)]);
-        // component c of the two halves' pieces: k = 8 ks + 4 fh + c
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[c], b[c], acc, 0, 0, 0);
-      }
+      for (int ks = 0; ks < 4; ++ks)
+        acc = mma_f32(l[ra * 8 + swzb(ra, 2 * ks + fh)], l[rb * 8 + swzb(rb, 2 * ks + fh)], acc);
       if (kt + 1 < KT) put((kt + 1) & 1);
       __syncthreads();
     }
   }
-  float *stage = reinterpret_cast<float *>(&ring[0][0]);
+  // the second group's sums join the first's
+  float *stage = reinterpret_cast<float *>(&ring[0][0][0]);
+  for (int g = 1; g >= 0; --g) {
+    if (grp == g)
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    stage[(wm * 32 + 8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * 32 + fr] = acc[e];
-  __syncthreads();
+      for (int e = 0; e < 16; ++e) {
+        float *p = stage + (wm * 32 + 8 * (e >> 2) + 4 * fh + (e & 3)) * SP + wn * 32 + fr;
+        *p = g == 1 ? acc[e] : *p + acc[e];
+      }
+    __syncthreads();
+  }
   finish_rows<4, 4, BNF, SP, 2>([&](int w) { return stage + w * 32 * SP; }, 0, 1, m0, n0, s_row,
                                 s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
+}
+
+// Tiles of 32 x 32 whose eight waves cut K, operands straight from memory:
+// where tiles of 64 x 64 would not fill the chip.
+constexpr int kF32Waves = 8;
+
+__global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
+    const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
+    const float *__restrict__ v, const int32_t *__restrict__ adapter,
+    const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
+    int NT) {
+  constexpr int BM = 32, BNF = 32, SP = BNF + 4;
+  __shared__ float red[kF32Waves][BM * SP];
+  __shared__ int s_row[BM], s_ad[BM];
+  __shared__ int s_hom[1];
+  const TileAt at = tile_at(blockIdx.x, MT, NT);
+  if (at.mt < 0) return;
+  const int m0 = at.mt * BM, n0 = at.nt * BNF;
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  const int fr = lane & 31, fh = lane >> 5;
+  if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
+  if (tid == 0) s_hom[0] = 0;
+  f32x16 acc = f32x16{};
+  __syncthreads();
+  if (W) {
+    const int KP = K / 4;
+    const u32x4 *xp = reinterpret_cast<const u32x4 *>(x + (size_t)s_row[fr] * K * 4);
+    const u32x4 *wp = reinterpret_cast<const u32x4 *>(W + (size_t)min(n0 + fr, N - 1) * ldw * 4);
+    // a wave takes whole lines of 8 pieces
+    constexpr int U = 4, CHUNK = 2 * U * kF32Waves;
+    int p0 = 0;
+    for (; p0 + CHUNK <= KP; p0 += CHUNK) {
+      u32x4 xa[U], wa[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        xa[u] = xp[p0 + (wv * U + u) * 2 + fh];
+        wa[u] = wp[p0 + (wv * U + u) * 2 + fh];
+      }
+      __builtin_amdgcn_sched_barrier(0);  // every load of the chunk is issued first
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc = mma_f32(xa[u], wa[u], acc);
+    }
+    if (p0 < KP) {  // zeros behind K
+      u32x4 xa[U], wa[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        xa[u] = load_piece(xp, p0 + (wv * U + u) * 2 + fh, KP);
+        wa[u] = load_piece(wp, p0 + (wv * U + u) * 2 + fh, KP);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc = mma_f32(xa[u], wa[u], acc);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) red[wv][(8 * (e >> 2) + 4 * fh + (e & 3)) * SP + fr] = acc[e];
+  __syncthreads();
+  for (int i = tid; i < BM * BNF; i += kF32Waves * kWave) {
+    const int o = (i / BNF) * SP + i % BNF;
+    float sum = red[0][o];
+#pragma unroll
+    for (int w = 1; w < kF32Waves; ++w) sum += red[w][o];
+    red[0][o] = sum;
+  }
+  __syncthreads();
+  finish_rows<4, 4, BNF, SP, 1>([&](int) { return &red[0][0]; }, 0, 1, m0, n0, s_row, s_ad, s_hom,
+                                W == nullptr, F, v, T, N, r, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -663,7 +742,7 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
   for (int b = 0; b < MB; ++b) acc[b] = f32x4{};
   // a wave takes two neighbouring groups of 4 pieces (whole 128-byte lines)
   // out of each 16; the last, partial chunk reads zeros behind K
-  constexpr int U = MB <= 2 ? 8 : 4;
+  constexpr int U = MB == 1 ? 16 : 8;
   constexpr int CHUNK = U * kRowWaves * 4;  // pieces that the workgroup takes at once
   auto multiply = [&](const u32x4 (&wa)[U], const u32x4 (&xa)[U][MB]) {
     __builtin_amdgcn_sched_barrier(0);  // every load of the chunk is issued first
@@ -725,8 +804,10 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
   }
 }
 
-// rows up to which expand_rows_kernel runs (bf16 with a W)
-constexpr int kExpandRowsMax = 64;
+// Rows up to which expand_rows_kernel runs (bf16 with a W).  Every workgroup
+// reads all of x, so above that the tiles are faster (N and K 4096: 64 rows
+// 27.7 us here, 80 rows 23.4 us in tiles; 32 rows 18.9 us here).
+constexpr int kExpandRowsMax = 32;
 
 // Tile shapes of the bf16 kernels, and what a 64-deep K step and the rest of a
 // tile take on a CU, in ns: measured with one tile per CU on 96 to 4096 rows,
@@ -757,11 +838,11 @@ int pick_tile(int T, int N, int K, bool with_w, int cus) {
 }
 
 template <class Kernel, class... More>
-void launch_tiles(Kernel kernel, int BM, int BNT, const char *x, const char *W, int ldw,
+void launch_tiles(Kernel kernel, int threads, int BM, int BNT, const char *x, const char *W, int ldw,
                   const char *F, const float *v, const int32_t *adapter, const int32_t *order, int T,
                   int N, int K, int r, int n, char *y, hipStream_t s, More... more) {
   const int MT = (T + BM - 1) / BM, NT = (N + BNT - 1) / BNT;
-  hipLaunchKernelGGL(kernel, dim3(tile_grid(MT, NT)), dim3(256), 0, s, x, W, ldw, F, v, adapter,
+  hipLaunchKernelGGL(kernel, dim3(tile_grid(MT, NT)), dim3(threads), 0, s, x, W, ldw, F, v, adapter,
                      order, T, N, K, r, n, y, MT, NT, more...);
 }
 
@@ -775,17 +856,16 @@ void launch_bf16(const char *x, const char *W, int ldw, const char *F, const flo
   hipLaunchKernelGGL((expand_rows_kernel<OS, MB>), grid, block, 0, s, x, W, ldw, F, v, adapter, T, \
                      N, K, r, n, y)
     if (T <= 16) MOE_ROWS(1);
-    else if (T <= 32) MOE_ROWS(2);
-    else MOE_ROWS(4);
+    else MOE_ROWS(2);
 #undef MOE_ROWS
     return;
   }
   const int rot = T <= 128;
 #define MOE_TILES(kernel, BM, BNT) \
-  launch_tiles(kernel, BM, BNT, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y, s, rot)
+  launch_tiles(kernel, 256, BM, BNT, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y, s, rot)
   switch (pick_tile(T, N, K, W != nullptr, cus)) {
     case 0:
-      launch_tiles(expand_big_kernel<OS>, 256, 256, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y,
+      launch_tiles(expand_big_kernel<OS>, 256, 256, 256, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y,
                    s);
       break;
     case 1: MOE_TILES((expand_ring_kernel<OS, 128, 128, 2, 2, 4>), 128, 128); break;
@@ -804,8 +884,15 @@ hipError_t launch_lora_expand(const void *x, const void *W, int ldw, const void 
   const char *xb = static_cast<const char *>(x), *wb = static_cast<const char *>(W),
              *fb = static_cast<const char *>(F);
   char *yb = static_cast<char *>(y);
-  if (dt == MOE_F32)
-    launch_tiles(expand_f32_kernel, 64, 64, xb, wb, ldw, fb, v, adapter, order, T, N, K, r, n, yb, s);
+  if (dt == MOE_F32) {
+    const long long tiles = (long long)((T + 63) / 64) * ((N + 63) / 64);
+    if (tiles < cus)
+      launch_tiles(expand_f32_small_kernel, kF32Waves * moe::kWave, 32, 32, xb, wb, ldw, fb, v, adapter,
+                   order, T, N, K, r, n, yb, s);
+    else
+      launch_tiles(expand_f32_kernel, kF32Threads, 64, 64, xb, wb, ldw, fb, v, adapter, order, T, N, K,
+                   r, n, yb, s);
+  }
   else if (y_dt == MOE_F32)
     launch_bf16<4>(xb, wb, ldw, fb, v, adapter, order, T, N, K, r, n, yb, cus, s);
   else

@@ -46,11 +46,11 @@ struct LoraUnit {
 };
 
 // Slices of K that the sorted shrink cuts a tile into: enough workgroups for
-// two per CU, at least 1 KB of every row each.
+// one per CU, at least 1 KB of every row each.
 inline int lora_shrink_slices(int T, int row_bytes, int r) {
   const int tiles = (T + moe::kShrinkTile - 1) / moe::kShrinkTile * (r > 64 ? 2 : 1);
   int s = 1;
-  while (s < moe::kShrinkSlices && tiles * s < 512 && row_bytes / (2 * s) >= 1024) s *= 2;
+  while (s < moe::kShrinkSlices && tiles * s < 256 && row_bytes / (2 * s) >= 1024) s *= 2;
   return s;
 }
 

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kPlanWaves *kWave) void lora_plan_kernel(
   const long long c0 = (long long)wv * chunk;
   const int t0 = (int)min(c0, (long long)T), t1 = (int)min(c0 + chunk, (long long)T);
   // the first rows' adapters stay in registers for both passes
-  constexpr int KEEP = 8;
+  constexpr int KEEP = 4;
   int mine[KEEP];
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
@@ -63,12 +63,37 @@ __global__ __launch_bounds__(kPlanWaves *kWave) void lora_plan_kernel(
     mine[i] = t < t1 ? (a >= 0 && a < n ? a : n) : -1;
   }
   for (int a = lane; a <= n; a += kWave) count[wv][a] = 0;  // (the wave's own)
+  // 64 rows at a time: the lanes that hold a row's adapter, by one ballot per
+  // bit of it.  The first of them counts for all (the rows of a prompt would
+  // queue at one counter).
+  auto lanes_of = [&](int a) {
+    unsigned long long same = __ballot(a >= 0);
+    for (int bit = 0; (n >> bit) != 0; ++bit) {
+      const unsigned long long ones = __ballot((a >> bit) & 1);
+      same &= (a >> bit) & 1 ? ones : ~ones;
+    }
+    return same;
+  };
+  auto take = [&](int a, unsigned long long same) {  // places for a's rows, or their number
+    const int first = a >= 0 ? __builtin_ctzll(same) : lane;
+    int at = 0;
+    if (a >= 0 && lane == first) at = atomicAdd(&count[wv][a], (int)__popcll(same));
+    return __shfl(at, first, kWave);
+  };
+  auto behind = [&](int t) {
+    const int a = adapter[min(t, T - 1)];
+    return t < t1 ? (a >= 0 && a < n ? a : n) : -1;
+  };
+  unsigned long long same[KEEP];
 #pragma unroll
   for (int i = 0; i < KEEP; ++i)
-    if (mine[i] >= 0) atomicAdd(&count[wv][mine[i]], 1);
-  for (int t = t0 + KEEP * kWave + lane; t < t1; t += kWave) {
-    const int a = adapter[t];
-    atomicAdd(&count[wv][a >= 0 && a < n ? a : n], 1);
+    if (t0 + i * kWave < t1) {
+      same[i] = lanes_of(mine[i]);
+      take(mine[i], same[i]);
+    }
+  for (int b = t0 + KEEP * kWave; b < t1; b += kWave) {
+    const int a = behind(b + lane);
+    take(a, lanes_of(a));
   }
   __syncthreads();
   // thread a: adapter a's rows, and its rows' places wave by wave
@@ -76,9 +101,7 @@ __global__ __launch_bounds__(kPlanWaves *kWave) void lora_plan_kernel(
 #pragma unroll
   for (int w = 0; w < kPlanWaves; ++w) c[w] = count[w][min(tid, n)];
 #pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) {
-    rows += tid < n ? c[w] : 0;
-  }
+  for (int w = 0; w < kPlanWaves; ++w) rows += tid < n ? c[w] : 0;
   const int nu = tid < n && units ? max(1, (rows + TS - 1) / TS) : 0;  // no rows: one unit of none
   Four all;
   const Four ex = block_scan({rows, (rows + kShrinkTile - 1) / kShrinkTile, nu, nu > 1 ? nu : 0}, s_w,
@@ -118,27 +141,16 @@ __global__ __launch_bounds__(kPlanWaves *kWave) void lora_plan_kernel(
   }
   if (tid == 0 && units) *n_units = all.v[2];
   __syncthreads();
-  // 64 rows at a time: the lanes of a row's adapter by one ballot per bit of
-  // it; the first of them takes their places
-  auto place = [&](int a, int t) {
-    unsigned long long same = __ballot(a >= 0);
-    for (int bit = 0; (n >> bit) != 0; ++bit) {
-      const unsigned long long ones = __ballot((a >> bit) & 1);
-      same &= (a >> bit) & 1 ? ones : ~ones;
-    }
-    const int first = a >= 0 ? __builtin_ctzll(same) : lane;
-    int at = 0;
-    if (a >= 0 && lane == first) at = atomicAdd(&count[wv][a], (int)__popcll(same));
-    at = __shfl(at, first, kWave);
-    if (a >= 0) order[at + __popcll(same & ((1ull << lane) - 1))] = t;
+  auto place = [&](int a, unsigned long long with, int t) {
+    const int at = take(a, with);
+    if (a >= 0) order[at + __popcll(with & ((1ull << lane) - 1))] = t;
   };
 #pragma unroll
   for (int i = 0; i < KEEP; ++i)
-    if (t0 + i * kWave < t1) place(mine[i], t0 + i * kWave + lane);
+    if (t0 + i * kWave < t1) place(mine[i], same[i], t0 + i * kWave + lane);
   for (int b = t0 + KEEP * kWave; b < t1; b += kWave) {
-    const int t = b + lane;
-    const int a = adapter[min(t, T - 1)];
-    place(t < t1 ? (a >= 0 && a < n ? a : n) : -1, t);
+    const int a = behind(b + lane);
+    place(a, lanes_of(a), b + lane);
   }
 }
 

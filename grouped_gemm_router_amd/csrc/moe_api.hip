@@ -366,9 +366,9 @@ moe_status_t lora_sizes(int T, int N, int K, int r, int n, moe_dtype_t dt) {
   if (!is_act(dt)) return MOE_ERR_UNSUPPORTED;
   if (K % 8 != 0 || r % 8 != 0 || r > MOE_LORA_MAX_RANK || n > MOE_LORA_MAX_ADAPTERS)
     return MOE_ERR_UNSUPPORTED;
-  // a launch has fewer than 2^32 threads: at most 2^23 tiles of 64 x 64
+  // a launch has fewer than 2^32 threads: at most 2^22 tiles of 64 x 64
   if (T > (1 << 24) || N > (1 << 20) || K > (1 << 20) ||
-      (long long)T * (N > K ? N : K) > (1ll << 35))
+      (long long)T * (N > K ? N : K) > (1ll << 34))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

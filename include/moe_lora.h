@@ -21,7 +21,7 @@
  * MOE_F32; products accumulate in fp32, and v and u are fp32.
  * Requires K % 8 == 0, r % 8 == 0, 8 <= r <= MOE_LORA_MAX_RANK,
  * 1 <= n <= MOE_LORA_MAX_ADAPTERS, T <= 2^24, N and K <= 2^20 and
- * T max(N, K) <= 2^35.
+ * T max(N, K) <= 2^34.
  */
 #ifndef MOE_LORA_H
 #define MOE_LORA_H
