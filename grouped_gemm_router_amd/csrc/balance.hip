@@ -11,8 +11,7 @@
 // Everything is one pass over the logits: HBM-bound on large batches,
 // latency-bound on small ones, so a batch of loads is always in flight before
 // the one before it is used, and the sums over a token's lanes are DPP.
-#include "moe_internal.h"
-#include "../../include/moe_balance.h"
+#include "balance_internal.h"
 
 namespace {
 

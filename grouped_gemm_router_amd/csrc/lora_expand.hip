@@ -12,8 +12,7 @@
 // many adapters every row reads its own adapter's rows of F on the vector
 // ALUs.  No row ever adds another adapter's values, not even multiplied by
 // zero: an infinity in one request's adapter stays in that request's rows.
-#include "gemm_bf16_tile.h"
-#include "lora_internal.h"
+#include "lora_tile.h"
 
 namespace {
 
@@ -569,7 +568,7 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
   _Pragma("unroll") for (int j = 0; j < NB; ++j)                                           \
     f.b[j] = __builtin_bit_cast(bf16x8, (slot)[rb[ks] + j * 256]);
 #define MOE_MMA(f)                             \
-  mfma_frag<MI, NB>(acc, f, MI);               \
+  mfma_frag<MI, NB>(acc, f);                   \
   interleave_mfma_ds_read<MI * NB, MI + NB>();
 // Step kt, whose first fragments are in f0: each 16-deep part is multiplied
 // while the next one's fragments are read.  Before the last part, every wave
@@ -645,9 +644,8 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// bf16, large batches: 256 x 256 tiles on the grouped GEMM's K loop (four
-// waves of 128 x 128, which reads half as many operand bytes from LDS per
-// multiply as 64 x 64).  K % 128 == 0.
+// bf16, large batches: 256 x 256 tiles (four waves of 128 x 128, which read
+// half as many operand bytes from LDS per multiply as 64 x 64).  K % 128 == 0.
 // ---------------------------------------------------------------------------
 template <int OS>
 __global__ __launch_bounds__(256, 1) void expand_big_kernel(
@@ -655,45 +653,35 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     const float *__restrict__ v, const int32_t *__restrict__ adapter,
     const int32_t *__restrict__ order, int T, int N, int K, int r, int n, char *__restrict__ y, int MT,
     int NT) {
-  constexpr int NW = 4, NWN = 2, MI = 4, NB = 4;
-  constexpr int SLOTS_A2 = BM_MAX * PIECES_B;
-  constexpr int IA = SLOTS_A2 / NW / 64, IB = SLOTS_B2 / NW / 64;
-  __shared__ u32x4 sA0[SLOTS_A2MAX], sA1[SLOTS_A2MAX];
-  __shared__ u32x4 sB0[SLOTS_B2], sB1[SLOTS_B2], sB2[SLOTS_B2];
+  constexpr int MI = kBigBlocks, NB = kBigBlocks;
+  __shared__ u32x4 sA0[kBigSlot], sA1[kBigSlot];
+  __shared__ u32x4 sB0[kBigSlot], sB1[kBigSlot], sB2[kBigSlot];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
-  const int m0 = at.mt * BM_MAX, n0 = at.nt * BN;
+  const int m0 = at.mt * kBig, n0 = at.nt * kBig;
   const int tid = threadIdx.x, lane = lane_id(),
             wv = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wv / NWN, wn = wv % NWN, fr = lane & 31, fh = lane >> 5;
+  const int wm = wv / 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
   // the tile's rows wait in the last B slot, which the K loop fills last
   int *const rows = reinterpret_cast<int *>(sB2);
-  load_row(rows, rows + BM_MAX, tid, m0, adapter, order, T, n);
+  load_row(rows, rows + kBig, tid, m0, adapter, order, T, n);
   __syncthreads();
-  const uint16_t *ga[IA], *gb[IB];
-  const int dma_a = wv * (SLOTS_A2 / NW), dma_b = wv * (SLOTS_B2 / NW);
+  const uint16_t *ga[kBigLoads], *gb[kBigLoads];
 #pragma unroll
-  for (int i = 0; i < IA; ++i) {
-    const int sl = dma_a + i * 64 + lane, row = sl / PIECES_B;
-    ga[i] = reinterpret_cast<const uint16_t *>(x) + (size_t)rows[row] * K +
-            swzb(row, sl % PIECES_B) * 8;
-  }
-#pragma unroll
-  for (int i = 0; i < IB; ++i) {
-    const int sl = dma_b + i * 64 + lane, row = sl / PIECES_B;
-    gb[i] = reinterpret_cast<const uint16_t *>(W) + (size_t)min(n0 + row, N - 1) * ldw +
-            swzb(row, sl % PIECES_B) * 8;
+  for (int i = 0; i < kBigLoads; ++i) {
+    const int sl = wv * (kBigSlot / 4) + i * 64 + lane, row = sl / 8, p = swzb(row, sl % 8);
+    ga[i] = reinterpret_cast<const uint16_t *>(x) + (size_t)rows[row] * K + p * 8;
+    gb[i] = reinterpret_cast<const uint16_t *>(W) + (size_t)min(n0 + row, N - 1) * ldw + p * 8;
   }
   f32x16 acc[MI][NB];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-  tile_k_loop<false, MI, NB, NWN, IA, IB>(acc, ga, gb, K / BK, dma_a, dma_b, wm, wn, fr, fh, MI, sA0,
-                                          sA1, sB0, sB1, sB2);
+  big_k_loop(acc, ga, gb, K / kBigK, wv, fr, fh, sA0, sA1, sB0, sB1, sB2);
   __syncthreads();  // every wave is done with the rings
-  int *const s_row = reinterpret_cast<int *>(sA0), *const s_ad = s_row + BM_MAX,
-             *const s_hom = s_ad + BM_MAX;
+  int *const s_row = reinterpret_cast<int *>(sA0), *const s_ad = s_row + kBig,
+             *const s_hom = s_ad + kBig;
   load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   __syncthreads();
   low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_row, s_ad, s_hom, wm * MI, lane == 0 && wn == 0,
@@ -707,9 +695,9 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        mine[(8 * (e >> 2) + 4 * fh + (e & 3)) * BN + wn * (NB * 32) + j * 32 + fr] = acc[i][j][e];
+        mine[(8 * (e >> 2) + 4 * fh + (e & 3)) * kBig + wn * (NB * 32) + j * 32 + fr] = acc[i][j][e];
     __syncthreads();
-    finish_rows<2, OS, BN, BN, 2>(
+    finish_rows<2, OS, kBig, kBig, 2>(
         [&](int w) { return reinterpret_cast<const float *>(w == 0 ? sB0 : sB1); }, i, MI, m0, n0,
         s_row, s_ad, s_hom, false, F, v, T, N, r, y);
   }

@@ -8,7 +8,7 @@
 
 #include <atomic>
 
-#include "../../include/moe_balance.h"
+#include "balance_internal.h"
 #include "lora_internal.h"
 #include "moe_internal.h"
 

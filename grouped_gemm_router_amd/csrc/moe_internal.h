@@ -342,18 +342,6 @@ size_t route_ws_bytes(int T, int d, int E);
 
 hipError_t launch_router_stats(const float *prob_sums, const int32_t *counts, int T, int E, int k,
                                float alpha, float *f, float *P, float *summary, hipStream_t s);
-
-size_t balance_loss_ws_bytes(int T, int E, int S);
-hipError_t launch_balance_loss(const float *logits, const int32_t *topk_idx, const int32_t *off,
-                               const uint8_t *mask, int T, int E, int k, int S, float alpha,
-                               int32_t *counts, float *probs, int32_t *tokens, float *loss, void *ws,
-                               hipStream_t s);
-hipError_t launch_route_backward(const float *logits, const int32_t *topk_idx, const float *dw,
-                                 bool renorm, const int32_t *counts, const int32_t *tokens,
-                                 float alpha, const float *d_loss, const int32_t *off,
-                                 const uint8_t *mask, int T, int E, int k, int S, float *d_logits,
-                                 hipStream_t s);
-
 // prob_sums: [ceil(T/16)][E] per-block sums of the softmax probabilities, or null
 hipError_t launch_route(const void *x, const void *w_router, int dt, const float *bias,
                         int T, int d, int E, int k, unsigned flags, float *logits,
