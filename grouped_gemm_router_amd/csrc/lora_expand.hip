@@ -10,8 +10,8 @@
 // terms (two for a bf16 y, three for an fp32 y, so that the product keeps 16
 // or 24 bits of v) and multiplied like 16 more columns of x.  In a block of
 // many adapters every row reads its own adapter's rows of F on the vector
-// ALUs.  No row ever adds another adapter's values, not even multiplied by
-// zero: an infinity in one request's adapter stays in that request's rows.
+// ALUs.  An infinity or NaN in one request's adapter stays in that request's
+// rows, and changes no bit of the others.
 #include "lora_tile.h"
 
 namespace {
@@ -80,127 +80,238 @@ __device__ __forceinline__ void st8(char *p, size_t i, int have, const float (&f
   }
 }
 
-// Eight ranks of the factor at F (rows of N) for each of the lane's columns.
-template <int NB>
-__device__ __forceinline__ void load_ranks(uint16_t (&w)[NB][8], const uint16_t *F, int N,
-                                           const int (&n)[NB]) {
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[nb][i] = F[(size_t)i * N + n[nb]];
-}
-
-// acc[nb] += v F of 32 rows, 16 ranks from j0: the lane's eight values of v
-// (zero where its ranks do not exist), split into TERMS, and its columns'
-// ranks w.
-template <int TERMS, int NB>
-__device__ __forceinline__ void mma_ranks(f32x16 (&acc)[NB], f32x4 v0, f32x4 v1,
-                                          const uint16_t (&w)[NB][8], bool in) {
-  float f[8];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    f[c] = in ? v0[c] : 0.f;
-    f[4 + c] = in ? v1[c] : 0.f;
-  }
-  bf16x8 va[TERMS];
-  split_bf16<TERMS>(f, va);
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    u32x4 q;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      q[c] = in ? (uint32_t)w[nb][2 * c] | ((uint32_t)w[nb][2 * c + 1] << 16) : 0u;
-    const bf16x8 b = __builtin_bit_cast(bf16x8, q);
-#pragma unroll
-    for (int k = 0; k < TERMS; ++k)
-      acc[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[k], b, acc[nb], 0, 0, 0);
-  }
-}
-
 // Adapters among 32 rows up to which they go through the matrix cores one
 // after the other.
 constexpr int kBlockKinds = 6;
 
-// The low-rank part of a wave's MI x NB blocks on the matrix cores, 16 ranks
-// a step; s_hom says for which blocks it is done here.
-//   * a block whose 32 rows share an adapter: acc[i][nb] += v F;
-//   * a block of a few adapters: all 32 rows times each adapter's factor into
-//     registers of their own, of which each row adds its own adapter's.
-// s_row, s_ad: the tile's rows and adapters (-1 for none); first: the wave's
-// first row block; n0: its first column.
-template <int TERMS, int MI, int NB>
-__device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], const int *s_row,
-                                                const int *s_ad, int *s_hom, int first, bool tell,
-                                                int n0, const char *F, const float *v, int N, int r,
-                                                int fr, int fh) {
-  int a[MI];
-  bool hom[MI], few[MI], any = false;
-  const float *vr[MI];
-  int n[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) n[j] = min(n0 + j * 32 + fr, N - 1);
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int row = (first + i) * 32 + fr, mine = s_ad[row];
-    const int a0 = __builtin_amdgcn_readfirstlane(mine);
-    hom[i] = a0 >= 0 && __all(mine == a0);
-    a[i] = max(a0, 0);
-    vr[i] = v + (size_t)s_row[row] * r;
-    any = any || hom[i];
-    int kinds = 0;
-    for (unsigned left = (unsigned)__ballot(mine >= 0); left; ++kinds)
-      left &= ~(unsigned)__ballot(mine == __builtin_amdgcn_readlane(mine, __builtin_ctz(left)));
-    few[i] = !hom[i] && kinds > 0 && kinds <= kBlockKinds;
-    if (tell) s_hom[first + i] = hom[i] || few[i];
-  }
-  const uint16_t *Fw = reinterpret_cast<const uint16_t *>(F);
-  // r is a multiple of 8: a lane's eight ranks of a step exist or not.  Where
-  // they do not, the last eight are loaded and both operands are zero.
-  for (int j0 = 0; any && j0 < r; j0 += 16) {
-    const bool in = j0 + 8 * fh < r;
-    const int j = min(j0 + 8 * fh, r - 8);
-    f32x4 v0[MI], v1[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      v0[i] = *reinterpret_cast<const f32x4 *>(vr[i] + j);
-      v1[i] = *reinterpret_cast<const f32x4 *>(vr[i] + j + 4);
+// The adapters of a tile's row blocks.  count: how many a block of 32 rows
+// has, 0 if it does not go through the matrix cores (none, or more than
+// kBlockKinds).  Its k-th adapter is that of slot base + k; neighbouring
+// blocks share a slot where the one ends with the adapter that the next one
+// begins with.
+struct TileKinds {
+  int count[8], base[8], ad[8][8], slot_ad[8 * kBlockKinds], slots;
+  int bad;  // a staged factor holds an infinity or NaN
+};
+
+// by the whole workgroup of four waves; every thread may read it on return
+__device__ __forceinline__ void find_kinds(TileKinds &tk, const int *s_ad, int blocks, int wv) {
+  const int lane = lane_id();
+  for (int blk = wv; blk < blocks; blk += 4) {
+    const int mine = s_ad[blk * 32 + (lane & 31)];
+    unsigned left = (unsigned)__ballot(mine >= 0);
+    int kinds = 0, ids = -1;  // lane k: the k-th adapter
+    while (left && kinds <= kBlockKinds) {
+      const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+      ids = lane == kinds ? a : ids;
+      left &= ~(unsigned)__ballot(mine == a);
+      ++kinds;
     }
-    uint16_t w[NB][8];
-    load_ranks<NB>(w, Fw + ((size_t)a[0] * r + j) * N, N, n);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      // the rows of a prompt share the factor's fragments from block to block
-      if (i > 0 && a[i] != a[i - 1]) load_ranks<NB>(w, Fw + ((size_t)a[i] * r + j) * N, N, n);
-      if (hom[i]) mma_ranks<TERMS, NB>(acc[i], v0[i], v1[i], w, in);
+    if (lane < 8) tk.ad[blk][lane] = ids;
+    if (lane == 0) tk.count[blk] = kinds <= kBlockKinds ? kinds : 0;
+  }
+  __syncthreads();
+  if (wv == 0) {
+    const int blk = lane >> 3, k = lane & 7, bc = min(blk, blocks - 1);
+    const int cnt = blk < blocks ? tk.count[bc] : 0, mine = tk.ad[bc][k];
+    const int before = bc > 0 ? tk.count[bc - 1] : 0;
+    const int shares =
+        cnt > 0 && before > 0 && tk.ad[max(bc - 1, 0)][max(before - 1, 0)] == tk.ad[bc][0];
+    int total;
+    const int sum = wave_exclusive_scan(k == 0 ? cnt - shares : 0, &total);
+    const int base = __shfl(sum, lane & ~7, kWave) - shares;
+    if (k < cnt) tk.slot_ad[base + k] = mine;  // (a shared slot: the same value twice)
+    if (k == 0 && blk < blocks) tk.base[blk] = base;
+    if (lane == 0) {
+      tk.slots = total;
+      tk.bad = 0;
     }
   }
+  __syncthreads();
+}
+
+// The low-rank part of a tile's blocks on the matrix cores (those with a
+// count in tk), BM x BN on 4 waves of MI x NB blocks: acc[i][nb] += v F for
+// each of a block's adapters, the rows of v that are not its own as zeros.
+// (Where a factor is not finite, zeros would not do: then the sums of those
+// rows are kept aside.  The others' come out the same bit for bit.)
+//
+// v, split into its bf16 terms, and the adapters' rows of F (the tile's
+// columns) are staged in LDS as the matrix cores' fragments, up to RC ranks of
+// all the tile's adapters at once.  What counts here is the number of
+// instructions: the code runs once a tile, from beyond the instruction cache,
+// where it arrives at some 50 ns per 64 bytes (measured).  Fragments built from
+// single elements took 9 us a tile for 16 ranks on 256 x 256, and for 32 ranks
+// of 2 to 3 adapters a block on 128 x 128.
+//
+// v_of(row): 256 bytes for a row of the tile; slab_of(i), i < NSLAB: SLAB
+// bytes each.  s_row, s_ad: the tile's rows and adapters (-1 for none).
+// Called by the whole workgroup; other waves may still read what is staged on
+// return.
+template <int TERMS, int MI, int NB, int BM, int BN, int NSLAB, int SLAB, class VOf, class SlabOf>
+__device__ __forceinline__ void low_rank_blocks(f32x16 (&acc)[MI][NB], TileKinds &tk,
+                                                const int *s_row, const int *s_ad, int wm, int wn,
+                                                VOf v_of, SlabOf slab_of, int n0, const char *F,
+                                                const float *v, int N, int r) {
+  const int tid = threadIdx.x, lane = lane_id(), fr = lane & 31, fh = lane >> 5;
+  constexpr int NT = 256, CG = BN / 8;  // threads; groups of 8 columns
+  // ranks that are staged at once, in eights: the terms of a row of v are at
+  // most 16 pieces
+  constexpr int RO = TERMS == 2 ? 8 : 4, RC = 8 * RO;
+  static_assert(NSLAB <= 3, "slab() counts up to three");
+  static_assert(SLAB >= RC * BN * 2, "a chunk of an adapter's ranks must fit a slab");
+  const int slots = __builtin_amdgcn_readfirstlane(tk.slots);
+  const uint16_t *const Fw = reinterpret_cast<const uint16_t *>(F);
+  // column c of a slab's row of eight ranks: the threads of the transposition
+  // write 8 columns apart, to distinct banks
+  auto place = [](int c) { return c ^ ((c >> 3) & 7); };
+  int at[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) at[nb] = fh * BN + place(wn * (NB * 32) + nb * 32 + fr);
+  // the wave's blocks: the lane's row's adapter, and in lane k the k-th one
+  int mine[MI], ids[MI], count[MI], base0[MI];
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    if (!few[i]) continue;
-    const int mine = s_ad[(first + i) * 32 + fr];
-    unsigned todo = (unsigned)__ballot(mine >= 0);
-    while (todo) {
-      const int who = __builtin_amdgcn_readlane(mine, __builtin_ctz(todo));
-      const unsigned same = (unsigned)__ballot(mine == who);
-      todo &= ~same;
-      f32x16 own[NB];
+    const int blk = wm * MI + i;
+    mine[i] = s_ad[blk * 32 + fr];
+    ids[i] = tk.ad[blk][lane & 7];
+    count[i] = tk.count[blk];
+    base0[i] = tk.base[blk];
+  }
+  for (int rc = 0; slots > 0 && rc < r; rc += RC) {
+    // eights of ranks: those of the chunk, and the same with a zero one to make
+    // whole steps of 16
+    const int ro = min(RO, (r - rc) / 8), oc = (ro + 1) & ~1;
+    const int per = SLAB / (oc * BN * 16), inv = (65536 + oc - 1) / oc;
+    auto slab = [&](int slot) {
+      const int i = (slot >= per) + (NSLAB > 2 && slot >= 2 * per);
+      return slab_of(i) + (slot - i * per) * oc * BN;
+    };
+    for (int first = 0; first < slots; first += NSLAB * per) {
+      const int ns = min(NSLAB * per, slots - first);
+      if (rc > 0 || first > 0) __syncthreads();  // what is staged has been used
+      const int vn = first == 0 ? BM * oc : 0, fn = ns * oc * CG;
+      constexpr int U = 2;
+#pragma unroll 1
+      for (int b = tid; b - tid < fn || b - tid < (vn + U - 1) / U; b += NT) {
+        // eight ranks of eight columns
+        const int fi = min(b, fn - 1), cg = fi % CG, rest = fi / CG;
+        const int slot = (rest * inv) >> 16, o = rest - slot * oc;  // (rest is below 100: exact)
+        const uint16_t *const f0 =
+            Fw + ((size_t)tk.slot_ad[first + slot] * r + rc + min(o, ro - 1) * 8) * N;
+        const int c = n0 + cg * 8;
+        u32x4 q[8];
+        if (N % 8 == 0) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) own[nb] = f32x16{};
-      for (int j0 = 0; j0 < r; j0 += 16) {
-        const bool in = j0 + 8 * fh < r;
-        const int j = min(j0 + 8 * fh, r - 8);
-        uint16_t w[NB][8];
-        load_ranks<NB>(w, Fw + ((size_t)who * r + j) * N, N, n);
-        mma_ranks<TERMS, NB>(own, *reinterpret_cast<const f32x4 *>(vr[i] + j),
-                             *reinterpret_cast<const f32x4 *>(vr[i] + j + 4), w, in);
+          for (int i = 0; i < 8; ++i)
+            q[i] = *reinterpret_cast<const u32x4 *>(f0 + (size_t)i * N + min(c, N - 8));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              q[i][h] = (uint32_t)f0[(size_t)i * N + min(c + 2 * h, N - 1)] |
+                        ((uint32_t)f0[(size_t)i * N + min(c + 2 * h + 1, N - 1)] << 16);
+        }
+        // eight ranks of U rows
+        f32x4 v0[U], v1[U];
+        int row[U], ov[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = min((b - tid) * U + u * NT + tid, BM * oc - 1);
+          ov[u] = i / BM;
+          row[u] = i % BM;
+          const float *const vr = v + (size_t)s_row[row[u]] * r + rc + min(ov[u], ro - 1) * 8;
+          v0[u] = *reinterpret_cast<const f32x4 *>(vr);
+          v1[u] = *reinterpret_cast<const f32x4 *>(vr + 4);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // every load is issued first
+        if (first == 0) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float f[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) f[h] = ov[u] < ro ? (h < 4 ? v0[u][h] : v1[u][h - 4]) : 0.f;
+            bf16x8 t[TERMS];
+            split_bf16<TERMS>(f, t);
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+              v_of(row[u])[(k * RO + ov[u]) ^ (row[u] & 15)] = __builtin_bit_cast(u32x4, t[k]);
+          }
+        }
+        unsigned bad = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            q[i][h] = o < ro ? q[i][h] : 0u;
+            bad |= (q[i][h] & 0x7f807f80u) + 0x00800080u;  // an exponent of ones carries
+          }
+        if (b < fn) {
+          u32x4 *const to = slab(slot) + o * BN;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {  // column e: rank pairs into words
+            const unsigned sel = (e & 1) ? 0x07060302u : 0x05040100u;
+            u32x4 w;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              w[d] = __builtin_amdgcn_perm(q[2 * d + 1][e >> 1], q[2 * d][e >> 1], sel);
+            to[place(cg * 8 + e)] = w;
+          }
+          if (bad & 0x80008000u) tk.bad = 1;
+        }
       }
-      // register e holds row 8 (e / 4) + 4 fh + e % 4
-      const unsigned rows = same >> (4 * fh);
+      __syncthreads();
+      const bool finite = __builtin_amdgcn_readfirstlane(tk.bad) == 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const bool takes = (rows >> (8 * (e >> 2) + (e & 3))) & 1;
+      for (int i = 0; i < MI; ++i) {
+        const int row = (wm * MI + i) * 32 + fr;
+        const int num = __builtin_amdgcn_readfirstlane(count[i]);
+        const int base = __builtin_amdgcn_readfirstlane(base0[i]) - first;
+        const u32x4 *const vr = v_of(row);
+#pragma unroll 1
+        for (int k = max(0, -base); k < num && base + k < ns; ++k) {
+          const u32x4 *const sl = slab(base + k);
+          const bool takes = mine[i] == __builtin_amdgcn_readlane(ids[i], k);
+          const unsigned same = (unsigned)__ballot(takes);
+          if (finite || same == ~0u) {
+#pragma unroll 1
+            for (int o = 0; o < oc; o += 2) {
+              u32x4 va[TERMS];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[i][nb][e] += takes ? own[nb][e] : 0.f;
+              for (int t = 0; t < TERMS; ++t) {
+                const u32x4 q = vr[(t * RO + o + fh) ^ (row & 15)];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) va[t][h] = takes ? q[h] : 0u;
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const bf16x8 w = __builtin_bit_cast(bf16x8, sl[o * BN + at[nb]]);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t)
+                  acc[i][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                      __builtin_bit_cast(bf16x8, va[t]), w, acc[i][nb], 0, 0, 0);
+              }
+            }
+            continue;
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            f32x16 all = acc[i][nb];
+#pragma unroll 1
+            for (int o = 0; o < oc; o += 2)
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t)
+                all = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, vr[(t * RO + o + fh) ^ (row & 15)]),
+                    __builtin_bit_cast(bf16x8, sl[o * BN + at[nb]]), all, 0, 0, 0);
+            // register e holds row 8 (e / 4) + 4 fh + e % 4
+            const unsigned rows = same >> (4 * fh);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[i][nb][e] = (rows >> (8 * (e >> 2) + (e & 3))) & 1 ? all[e] : acc[i][nb][e];
+          }
+        }
       }
     }
   }
@@ -501,7 +612,7 @@ __global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
 // ---------------------------------------------------------------------------
 __device__ u32x4 g_zero;
 
-template <int OS, int BM, int BNT, int WM, int WN, int NS>
+template <int OS, int BM, int BNT, int WM, int WN>
 __global__ __launch_bounds__(256) void expand_ring_kernel(
     const char *__restrict__ x, const char *__restrict__ W, int ldw, const char *__restrict__ F,
     const float *__restrict__ v, const int32_t *__restrict__ adapter,
@@ -509,13 +620,13 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
     int NT, int rot) {
   constexpr int MI = BM / WM / 32, NB = BNT / WN / 32;
   constexpr int IL = (BM + BNT) / 32;  // loads per wave and step
-  constexpr int SLOT = (BM + BNT) * 8, SP = BNT + 4;
+  constexpr int SLOT = (BM + BNT) * 8, SP = BNT + 4, NS = 4;
   static_assert(WM * WN == 4 && MI >= 1 && NB >= 1, "four waves of 32 x 32 blocks");
   static_assert(32 * SP * 4 <= SLOT * 16 && WM <= 2, "a staged row block must fit a slot");
-  static_assert(NS == 3 || NS == 4, "ring of three or four slots");
-  __shared__ u32x4 s0[SLOT], s1[SLOT], s2[SLOT], s3[NS == 4 ? SLOT : 1];
+  static_assert(BM * 16 <= SLOT, "64 floats for each row must fit a slot");
+  __shared__ u32x4 s0[SLOT], s1[SLOT], s2[SLOT], s3[SLOT];
   __shared__ int s_row[BM], s_ad[BM];
-  __shared__ int s_hom[BM / 32];
+  __shared__ TileKinds kinds;
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
   const int m0 = at.mt * BM, n0 = at.nt * BNT;
@@ -590,18 +701,12 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 #define MOE_PERIOD(kt, TAIL)             \
   MOE_STEP(s0, s1, kt, TAIL)             \
   MOE_STEP(s1, s2, (kt) + 1, TAIL)       \
-  if constexpr (NS == 4) {               \
-    MOE_STEP(s2, s3, (kt) + 2, TAIL)     \
-    MOE_STEP(s3, s0, (kt) + 3, TAIL)     \
-  } else {                               \
-    MOE_STEP(s2, s0, (kt) + 2, TAIL)     \
-  }
+  MOE_STEP(s2, s3, (kt) + 2, TAIL)       \
+  MOE_STEP(s3, s0, (kt) + 3, TAIL)
     MOE_ISSUE(s0, 0, true)
     MOE_ISSUE(s1, 1, true)
     MOE_ISSUE(s2, 2, true)
-    if constexpr (NS == 4) {
-      MOE_ISSUE(s3, 3, true)
-    }
+    MOE_ISSUE(s3, 3, true)
     wait_vmcnt<(NS - 1) * IL>();
     stage_barrier();
     Frag<MI, NB> f0, f1;
@@ -624,8 +729,11 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
   }
   __syncthreads();  // every wave is done with the ring
 
-  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_row, s_ad, s_hom, wm * MI, lane == 0 && wn == 0,
-                                           n0 + wn * (NB * 32), F, v, N, r, fr, fh);
+  find_kinds(kinds, s_ad, BM / 32, wv);
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB, BM, BNT, 3, SLOT * 16>(
+      acc, kinds, s_row, s_ad, wm, wn, [&](int row) { return s0 + row * 16; },
+      [&](int i) { return i == 0 ? s1 : i == 1 ? s2 : s3; }, n0, F, v, N, r);
+  if (kinds.slots > 0) __syncthreads();
   // 32 rows of every wave row at a time meet in LDS in fp32
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -639,7 +747,7 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
     __syncthreads();
     finish_rows<2, OS, BNT, SP, WM>(
         [&](int w) { return reinterpret_cast<const float *>(w == 0 ? s0 : s1); }, i, MI, m0, n0,
-        s_row, s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
+        s_row, s_ad, kinds.count, W == nullptr, F, v, T, N, r, y);
   }
 }
 
@@ -680,12 +788,16 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
   big_k_loop(acc, ga, gb, K / kBigK, wv, fr, fh, sA0, sA1, sB0, sB1, sB2);
   __syncthreads();  // every wave is done with the rings
-  int *const s_row = reinterpret_cast<int *>(sA0), *const s_ad = s_row + kBig,
-             *const s_hom = s_ad + kBig;
+  int *const s_row = rows, *const s_ad = rows + kBig;
+  TileKinds &kinds = *reinterpret_cast<TileKinds *>(rows + 2 * kBig);
   load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
   __syncthreads();
-  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB>(acc, s_row, s_ad, s_hom, wm * MI, lane == 0 && wn == 0,
-                                           n0 + wn * (NB * 32), F, v, N, r, fr, fh);
+  find_kinds(kinds, s_ad, kBig / 32, wv);
+  low_rank_blocks<OS == 2 ? 2 : 3, MI, NB, kBig, kBig, 2, kBigSlot * 16>(
+      acc, kinds, s_row, s_ad, wm, wn,
+      [&](int row) { return (row < kBig / 2 ? sA0 : sA1) + row % (kBig / 2) * 16; },
+      [&](int i) { return i == 0 ? sB0 : sB1; }, n0, F, v, N, r);
+  if (kinds.slots > 0) __syncthreads();
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     // 32 rows of both wave rows: 32 x 256 fp32 are one B slot
@@ -699,7 +811,7 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
     __syncthreads();
     finish_rows<2, OS, kBig, kBig, 2>(
         [&](int w) { return reinterpret_cast<const float *>(w == 0 ? sB0 : sB1); }, i, MI, m0, n0,
-        s_row, s_ad, s_hom, false, F, v, T, N, r, y);
+        s_row, s_ad, kinds.count, false, F, v, T, N, r, y);
   }
 }
 
@@ -856,9 +968,9 @@ void launch_bf16(const char *x, const char *W, int ldw, const char *F, const flo
       launch_tiles(expand_big_kernel<OS>, 256, 256, 256, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y,
                    s);
       break;
-    case 1: MOE_TILES((expand_ring_kernel<OS, 128, 128, 2, 2, 4>), 128, 128); break;
-    case 2: MOE_TILES((expand_ring_kernel<OS, 64, 128, 1, 4, 4>), 64, 128); break;
-    default: MOE_TILES((expand_ring_kernel<OS, 64, 64, 2, 2, 4>), 64, 64); break;
+    case 1: MOE_TILES((expand_ring_kernel<OS, 128, 128, 2, 2>), 128, 128); break;
+    case 2: MOE_TILES((expand_ring_kernel<OS, 64, 128, 1, 4>), 64, 128); break;
+    default: MOE_TILES((expand_ring_kernel<OS, 64, 64, 2, 2>), 64, 64); break;
   }
 #undef MOE_TILES
 }
