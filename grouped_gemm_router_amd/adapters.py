@@ -30,27 +30,18 @@ class AdaptedLinear:
         # row pitch as for the expert weights
         self.W = padded_weights(W[None])[0]
         self.W_t = padded_weights(W.t().contiguous()[None])[0] if grad else None
-        self._ws = {}
-
-    def _workspace(self, key, size):
-        ws = self._ws.get(key)
-        if ws is None or ws.numel() < size:
-            ws = torch.empty((max(size, 16),), dtype=torch.uint8, device=self.A.device)
-            self._ws[key] = ws
-        return ws
 
     def forward(self, x, adapter, *, out=None, out_dtype=None):
         """(y [T][N], v [T][r]): the projection of x [T][K] with the adapter
         of each row (adapter [T] int32, outside [0, n) for none), and the
-        low-rank vectors that backward() takes.  The workspace is the
-        object's: calls run one after the other on one stream."""
+        low-rank vectors that backward() takes.  Every call has a workspace
+        of its own from the allocator, so calls may run on several streams and
+        be captured into graphs."""
         T = x.shape[0]
         if out is None:
             out = torch.empty((T, self.N), dtype=out_dtype or x.dtype, device=x.device)
         v = torch.empty((T, self.r), dtype=torch.float32, device=x.device)
-        size = api.moe_lora_linear_workspace_size(T, self.N, self.K, self.r, self.n, x.dtype)
-        api.moe_lora_linear(x, self.A, self.B, self.scale, adapter, out, v, W=self.W,
-                            ws=self._workspace("forward", size))
+        api.moe_lora_linear(x, self.A, self.B, self.scale, adapter, out, v, W=self.W)
         return out, v
 
     __call__ = forward
@@ -65,8 +56,6 @@ class AdaptedLinear:
         dx = torch.empty((T, self.K), dtype=dy.dtype, device=dev)
         dA = torch.empty((self.n, self.r, self.K), dtype=f32, device=dev)
         dB = torch.empty((self.n, self.r, self.N), dtype=f32, device=dev)
-        size = api.moe_lora_backward_workspace_size(T, self.N, self.K, self.r, self.n, dy.dtype)
         api.moe_lora_linear_backward(dy, x, self.A, self.B, self.scale, adapter, v, u,
-                                     W_t=self.W_t, dx=dx, dA=dA, dB=dB,
-                                     ws=self._workspace("backward", size))
+                                     W_t=self.W_t, dx=dx, dA=dA, dB=dB)
         return dx, dA, dB

@@ -393,9 +393,13 @@ def _arg(t, name, dtype, *shape, device):
 
 
 def _raw_stream(stream, device) -> int:
-    """The hipStream_t of a stream, or of the device's current stream (read
-    without making a torch.cuda.Stream object of it)."""
+    """The hipStream_t of a stream, which must be the device's, or of the
+    device's current stream (read without making a torch.cuda.Stream object of
+    it)."""
     if stream is not None:
+        if stream.device_index != device:
+            raise ValueError("the stream is on GPU %d, the tensors on GPU %d"
+                             % (stream.device_index, device))
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)
 

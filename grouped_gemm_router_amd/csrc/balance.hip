@@ -233,7 +233,10 @@ __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
     const int lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
     if (lo >= b1 && !whole) break;
     const int ta = max(lo, b0), tb = min(hi, b1);
-    if (ta >= tb && !whole) continue;
+    if (ta >= tb && !whole) {  // empty: past all such at once
+      s += max(sequence_of(off + s, S - s, max(lo, b0)) - 1, 0);
+      continue;
+    }
     for (int e = tid; e < E; e += kThreadsP) s_c[e] = 0;
     if (tid == 0) s_n = 0;
     __syncthreads();
@@ -528,7 +531,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
     for (int s = s_first; s < S; ++s) {
       const int lo = off ? off[s] : 0, hi = off ? off[s + 1] : T;
       if (lo >= b1) break;
-      if (max(lo, b0) >= min(hi, b1)) continue;
+      if (max(lo, b0) >= min(hi, b1)) {  // empty: past all such at once
+        s += max(sequence_of(off + s, S - s, max(lo, b0)) - 1, 0);
+        continue;
+      }
       R bal;
       bal.fill(0.f);
       if (counts) {

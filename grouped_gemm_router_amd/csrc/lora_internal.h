@@ -57,7 +57,8 @@ inline int lora_shrink_slices(int T, int row_bytes, int r) {
 // Where the plan of a batch lies in a workspace, and the size of its units.
 // starts, tiles [n + 2]: each adapter's first row in the order and first
 // shrink tile, then those of the rows without an adapter, then the ends;
-// part: the slices of the shrink's tiles.
+// part: the slices of the shrink's sums, [rank group][slice][row of the
+// order][rank].
 struct LoraPlan {
   size_t order, starts, tiles, units, adapters, n_units, part, bytes;
   int TS, max_units, max_tiles;
@@ -81,7 +82,7 @@ inline LoraPlan lora_plan(int T, int N, int K, int r, int n, int es, bool backwa
   p.part = p.n_units + (backward ? 256 : 0);
   const int slices = lora_shrink_slices(T, (backward ? N : K) * es, r);
   const int RP = r <= 16 ? 16 : r <= 32 ? 32 : 64;
-  const size_t sums = (size_t)p.max_tiles * (r > 64 ? 2 : 1) * slices * moe::kShrinkTile * RP;
+  const size_t sums = (size_t)T * (r > 64 ? 2 : 1) * slices * RP;
   p.bytes = p.part + up(slices > 1 ? sums * 4 : 0);
   return p;
 }

@@ -183,7 +183,7 @@ template <int ES, int NR>
 __global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
     const char *__restrict__ x, const char *__restrict__ F, const float *__restrict__ scale,
     const int32_t *__restrict__ order, const int32_t *__restrict__ starts,
-    const int32_t *__restrict__ tiles, int max_tiles, int slices, int K, int r, int n,
+    const int32_t *__restrict__ tiles, int T, int slices, int K, int r, int n,
     float *__restrict__ part, float *__restrict__ v) {
   constexpr int RP = NR * 16;
   __shared__ float red[kTileWaves][kShrinkTile][RP + 1];
@@ -213,15 +213,15 @@ __global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
   else if (live <= 2) shrink_slice<ES, 2, NR>(x, F, s_row, K, r, a, j0, p0, p_end, wv, red[wv]);
   else shrink_slice<ES, kTileBlocks, NR>(x, F, s_row, K, r, a, j0, p0, p_end, wv, red[wv]);
   __syncthreads();
-  float *mine = part + (((size_t)blockIdx.y * max_tiles + tile) * slices + ks) * kShrinkTile * RP;
-  for (int i = tid; i < live * 16 * RP; i += kTileThreads) {
+  float *mine = part + (((size_t)blockIdx.y * slices + ks) * T + tr.first) * RP;
+  for (int i = tid; i < rows * RP; i += kTileThreads) {
     const int row = i / RP, j = i % RP;
     float sum = red[0][row][j];
 #pragma unroll
     for (int w = 1; w < kTileWaves; ++w) sum += red[w][row][j];
     if (slices > 1)
       mine[i] = sum;
-    else if (row < rows && j0 + j < r)
+    else if (j0 + j < r)
       v[(size_t)s_row[row] * r + j0 + j] = scale[a] * sum;
   }
 }
@@ -233,13 +233,13 @@ __global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
 __global__ __launch_bounds__(256) void shrink_sum_kernel(
     const float *__restrict__ part, const float *__restrict__ scale,
     const int32_t *__restrict__ order, const int32_t *__restrict__ starts,
-    const int32_t *__restrict__ tiles, int max_tiles, int slices, int RP, int r, int n,
+    const int32_t *__restrict__ tiles, int T, int slices, int RP, int r, int n,
     float *__restrict__ v) {
   const int tile = blockIdx.x / 4, j0 = blockIdx.y * RP;
   if (tile >= tiles[n + 1]) return;
   const TileRows tr = tile_rows(starts, tiles, n, tile);
   if (tr.a == n) return;
-  const float *all = part + ((size_t)blockIdx.y * max_tiles + tile) * slices * kShrinkTile * RP;
+  const float *all = part + ((size_t)blockIdx.y * slices * T + tr.first) * RP;
   const int r0 = (blockIdx.x % 4) * (kShrinkTile / 4);
   for (int i = threadIdx.x; i < kShrinkTile / 4 * RP; i += 256) {
     const int row = r0 + i / RP, j = i % RP;
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256) void shrink_sum_kernel(
     float p[kShrinkSlices];
 #pragma unroll
     for (int k = 0; k < kShrinkSlices; ++k)
-      p[k] = all[((size_t)min(k, slices - 1) * kShrinkTile + row) * RP + j];
+      p[k] = all[((size_t)min(k, slices - 1) * T + row) * RP + j];
     float sum = p[0];
 #pragma unroll
     for (int k = 1; k < kShrinkSlices; ++k) sum += k < slices ? p[k] : 0.f;
@@ -273,14 +273,14 @@ void launch_t(const void *x, const void *F, const float *scale, const int32_t *a
   float *part = reinterpret_cast<float *>(ws + p->part);
 #define MOE_SHRINK(NR)                                                                          \
   hipLaunchKernelGGL((shrink_tile_kernel<ES, NR>), grid, block, 0, s, xb, fb, scale, order, starts, \
-                     tiles, p->max_tiles, slices, K, r, n, part, v)
+                     tiles, T, slices, K, r, n, part, v)
   if (NR == 1) MOE_SHRINK(1);
   else if (NR == 2) MOE_SHRINK(2);
   else MOE_SHRINK(4);
 #undef MOE_SHRINK
   if (slices > 1)
     hipLaunchKernelGGL(shrink_sum_kernel, dim3((unsigned)p->max_tiles * 4, groups), dim3(256), 0, s,
-                       part, scale, order, starts, tiles, p->max_tiles, slices, 16 * NR, r, n, v);
+                       part, scale, order, starts, tiles, T, slices, 16 * NR, r, n, v);
 }
 
 }  // namespace

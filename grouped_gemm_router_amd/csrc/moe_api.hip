@@ -399,6 +399,8 @@ moe_status_t moe_lora_linear(const void *x, const void *W, int ldw, const void *
   if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(y) || !aligned16(v) ||
       !aligned4(scale) || !aligned4(adapter) || !pitch_ok(&ldw, K, dt, W))
     return MOE_ERR_INVALID;
+  // (in place only where W is elsewhere: every tile reads whole rows of x)
+  if (y == x && W) return MOE_ERR_INVALID;
   if (ws == nullptr && ws_bytes != 0) return MOE_ERR_INVALID;
   const size_t need = moe_lora_linear_workspace_size(T, N, K, r, n, dt);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -447,6 +449,8 @@ moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void 
   }
   if (ws_bytes < lora_wgrad_ws_bytes(T, N, K, r, n, size_of(dt))) return MOE_ERR_WORKSPACE;
   if (!aligned16(ws)) return MOE_ERR_INVALID;
+  // dx is written before dy and x are read for the last time
+  if (T > 0 && dx && (dx == dy || dx == x)) return MOE_ERR_INVALID;
   if (T == 0 && !dA) return MOE_OK;
   const hipStream_t s = as_stream(stream);
   const LoraPlan p = lora_plan(T, N, K, r, n, size_of(dt), true);

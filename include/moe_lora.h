@@ -19,6 +19,9 @@
  * then read each of them along rows only.  An adapter of a lower rank than r
  * has zero rows behind it.  x, W, A and B are of one type dt, MOE_BF16 or
  * MOE_F32; products accumulate in fp32, and v and u are fp32.
+ * An infinity or NaN in a row of x or in an adapter stays in the rows that
+ * use it and changes no bit of the others; in those rows it gives an infinity
+ * or a NaN, which of them is not specified.  Outputs must not overlap inputs.
  * Requires K % 8 == 0, r % 8 == 0, 8 <= r <= MOE_LORA_MAX_RANK,
  * 1 <= n <= MOE_LORA_MAX_ADAPTERS, T <= 2^24, N and K <= 2^20 and
  * T max(N, K) <= 2^34.

@@ -117,3 +117,17 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="GPU"):
         api.moe_lora_linear_backward(z(4, 16), z(4, 8), z(2, 8, 8), z(2, 8, 16), z(2),
                                      z(4, dtype=torch.int32), z(4, 8), z(4, 8))
+
+
+def test_lora_outputs_on_inputs_are_refused(lib):
+    """y over x is allowed only where the projection is not computed here, dx
+    never over dy or x."""
+    def f(x, y, W):
+        return lib.moe_lora_linear(x, W, 0, P, P, BF16, P, P, 16, 64, 64, 8, 2, y, BF16, P3, NUL, 0,
+                                   NUL)
+    assert f(P, P, P) == INVALID
+
+    def b(dy, x, dx):
+        return lib.moe_lora_linear_backward(dy, x, P, 0, P, P, BF16, P, P, P, 16, 64, 64, 8, 2, P, dx,
+                                            NUL, NUL, P, BIG, NUL)
+    assert b(P, P2, P) == INVALID and b(P, P2, P2) == INVALID

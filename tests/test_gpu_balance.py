@@ -413,3 +413,28 @@ def test_layer_balance_loss_and_route_backward(renorm):
     # every term is at most p (|g| + sum |g| p) <= 2 max |g|
     tol = 3 * (cfg.E + 60) * U * (2 * cfg.k * float(dw.abs().max()) + 2 * ALPHA * cfg.E / cfg.T)
     assert float((got - l.grad).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("E", [8, 100, 256])
+def test_many_empty_sequences(E):
+    """60000 sequences of which four have tokens: long runs of empty ones
+    before, between and behind them."""
+    T, S, k = 300, 60000, 4
+    lg, idx, _, _ = make(T, E, k, E)
+    off = torch.zeros(S + 1, dtype=torch.int32)
+    for at, end in ((777, 1), (778, 130), (41000, 131), (59990, 290)):
+        off[at + 1:] = end
+    check_loss(lg, idx, off, None)
+    check_backward(lg, idx, off, None, True)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(40, 8, 2), (70, 60, 6), (33, 256, 8), (50, 31, 5)])
+def test_gradient_of_closed_experts(T, E, k, renorm):
+    """Experts whose logit is -inf have probability and gradient 0, selected
+    or not."""
+    lg, idx, _, _ = make(T, E, k, 3 * T + E)
+    lg[:, 1] = lg[::3, E - 1] = float("-inf")
+    idx[::2, k - 1] = 1
+    got = check_backward(lg, idx, None, None, renorm)
+    assert (got[:, 1] == 0).all() and (got[::3, E - 1] == 0).all()

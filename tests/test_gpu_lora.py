@@ -495,3 +495,82 @@ def test_refusals_on_the_gpu():
         call(y=y.half())
     torch.cuda.synchronize()
     assert np.isfinite(float(c.g_x.float().sum()))
+
+
+# sorted batches whose 32-row blocks hold one to six adapters: ranks behind one
+# staged chunk (72, 128), an odd rank of eights, odd N, more adapters in a tile
+# than are staged at once, tiles of every size
+@pytest.mark.parametrize("out_dt", [BF, F32])
+@pytest.mark.parametrize("T,N,K,r,n", [
+    (600, 1000, 512, 72, 40), (700, 1200, 256, 128, 12), (1500, 1111, 256, 64, 100),
+    (2100, 3000, 256, 40, 200), (5000, 4096, 128, 128, 400), (300, 2050, 1024, 128, 30)])
+def test_blocks_of_a_few_adapters(T, N, K, r, n, out_dt):
+    print("lora few", T, N, K, r, n, out_dt, flush=True)
+    c = Case(T, N, K, r, n, BF, "mixed", T).gpu()
+    y0, v0 = check_forward(c, out_dt)
+    # an adapter that is not finite shares blocks and tiles with others, and
+    # changes no bit of them
+    c.g_A[n // 2], c.g_B[n // 2] = float("nan"), float("inf")
+    y1, v1 = forward(c, out_dt)
+    keep = (c.adapter != n // 2).to(DEV)
+    assert not keep.all()
+    assert torch.equal(y0[keep], y1[keep]) and torch.equal(v0[keep], v1[keep])
+    assert not torch.isfinite(y1[~keep].float()).any()
+
+
+def test_adapted_linear_graph_beside_larger_calls():
+    """A captured call keeps what it needs: eager calls of other, larger
+    batches of the same object between its replays, on two streams, change
+    nothing of it, nor it of them."""
+    from grouped_gemm_router_amd.adapters import AdaptedLinear
+    small = [Case(200, 512, 2048, 32, 9, BF, "mixed", i).gpu() for i in range(4)]
+    large = Case(1500, 512, 2048, 32, 9, BF, "mixed", 9).gpu()
+    s0 = small[0]
+    lin = AdaptedLinear(s0.g_W, s0.g_A, s0.g_B, s0.g_scale, grad=True)
+
+    def step(c):
+        y, v = lin(c.g_x, c.g_adapter)
+        return (y, v, *lin.backward(c.g_dy, c.g_x, c.g_adapter, v))
+
+    def same(p, q):
+        assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+    want = [step(c) for c in small]
+    want_large = step(large)
+    st = Case(200, 512, 2048, 32, 9, BF, "mixed", 0).gpu()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(st)
+    side = torch.cuda.Stream()
+    for i in (1, 2, 3, 0):
+        for k in ("x", "adapter", "dy"):
+            getattr(st, "g_" + k).copy_(getattr(small[i], "g_" + k))
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            beside = step(large)
+        again = step(large)
+        torch.cuda.synchronize()
+        same(want[i], out)
+        same(want_large, beside)
+        same(want_large, again)
+
+
+def test_workspace_grows_with_the_rows():
+    """The sums' slices take T r floats each, however many adapters there are."""
+    a = api()
+    for T, n in ((1024, 1024), (128, 1024), (4096, 16)):
+        size = a.moe_lora_linear_workspace_size(T, 14336, 4096, 64, n, BF)
+        assert size <= 8 * T * 64 * 4 + 8 * T + 16 * n + 4096, (T, n, size)
+
+
+def test_refuses_another_devices_stream():
+    class Other:
+        device_index, cuda_stream = 1, 0
+    a = api()
+    c = Case(20, 64, 128, 8, 2, BF, "mixed", 0).gpu()
+    y, v = torch.empty((20, 64), dtype=BF, device=DEV), torch.empty((20, 8), device=DEV)
+    with pytest.raises(ValueError, match="stream"):
+        a.moe_lora_linear(c.g_x, c.g_A, c.g_B, c.g_scale, c.g_adapter, y, v, W=c.g_W,
+                          ws=torch.empty(16, dtype=torch.uint8, device=DEV), stream=Other())
