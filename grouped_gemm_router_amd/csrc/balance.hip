@@ -165,11 +165,6 @@ __device__ __forceinline__ void softmax_row(R &x) {
   for (int i = 0; i < R::V; ++i) x.v[i] *= inv;
 }
 
-// tokens in flight per token slot: enough loads to cover the latency without
-// running out of registers
-template <class R>
-constexpr int unroll_of() { return R::V <= 4 ? 4 : (R::V <= 8 ? 2 : 1); }
-
 // ---------------------------------------------------------------------------
 // loss, first launch: block b (C tokens) writes, for every sequence s that
 // has tokens in it, slot b + s: the sums of the probabilities, the counts
@@ -190,7 +185,7 @@ __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
     const int32_t *__restrict__ off, const uint8_t *__restrict__ mask, int T, int E, int k, int S,
     int C, float alpha, float *__restrict__ slot_p, int32_t *__restrict__ slot_c,
     int32_t *__restrict__ slot_n, int32_t *__restrict__ ticket, LossOut out) {
-  constexpr int U = unroll_of<R>(), L = R::L, nq = kWave / L;
+  constexpr int L = R::L, nq = kWave / L;
   __shared__ float s_p[kWavesP][MOE_MAX_EXPERTS];
   __shared__ int s_c[MOE_MAX_EXPERTS];
   __shared__ int s_n;
@@ -201,19 +196,19 @@ __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
   const bool whole = gridDim.x == 1 && S == 1;
   if (b == 0 && tid == 0) *ticket = 0;
   constexpr int step = kWavesP * nq;  // token slots of the workgroup
-  // A batch is U tokens of every slot.  The first one is loaded before
-  // anything else is looked up: which tokens take part in which sequence is
-  // decided when its probabilities are there.
-  R x[U];
-  bool on[U];
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * step, tc = max(min(t, b1 - 1), 0);
-      if (b1 > b0) x[u].load(logits + (size_t)tc * E, l, E);
-      on[u] = t < b1;
-      if (mask) on[u] = on[u] && mask[tc];
-    }
+  // A batch is one token of every slot: the other waves of the CU cover its
+  // latency, in less code than several tokens a lane (which arrives slower
+  // than the data; 32749 tokens of 256 experts: 17.4 us with four, 16.0 with
+  // one).  The first one is loaded before anything else is looked up: which
+  // tokens take part in which sequence is decided when its probabilities are
+  // there.
+  R x;
+  bool on = false;
+  auto load = [&](int t) {
+    const int tc = max(min(t, b1 - 1), 0);
+    if (b1 > b0) x.load(logits + (size_t)tc * E, l, E);
+    on = t < b1;
+    if (mask) on = on && mask[tc];
   };
   const int slot = b0 + wv * nq + q;  // the lane's first token
   load(slot);
@@ -248,19 +243,15 @@ __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
     float acc[R::V];
 #pragma unroll
     for (int i = 0; i < R::V; ++i) acc[i] = 0.f;
-    for (int t0 = slot; t0 - q < b1; t0 += U * step) {
-      if (!first) load(t0);
-      first = b1 - b0 <= U * step;  // the block is one batch: it stays loaded
+    for (int t = slot; t - q < b1; t += step) {
+      if (!first) load(t);
+      first = b1 - b0 <= step;  // the block is one batch: it stays loaded
+      const bool in = on && t >= ta && t < tb;
+      n_mine += __popcll(__ballot(in && l == 0));
+      R p = x;
+      softmax_row(p);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * step;
-        const bool in = on[u] && t >= ta && t < tb;
-        n_mine += __popcll(__ballot(in && l == 0));
-        R p = x[u];
-        softmax_row(p);
-#pragma unroll
-        for (int i = 0; i < R::V; ++i) acc[i] += in ? p.v[i] : 0.f;
-      }
+      for (int i = 0; i < R::V; ++i) acc[i] += in ? p.v[i] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < R::V; ++i) {
@@ -443,6 +434,13 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Tokens in flight per token slot: few, so that the code, which runs once a
+// workgroup and arrives slower than the data, is short (4096 tokens of 8
+// experts: 6.8 us with four, 4.8 with two, 3.9 with one; 16381 of 256: 12.9,
+// 12.5, 13.3).
+template <class R>
+constexpr int backward_batch() { return R::L >= 32 && R::V <= 8 ? 2 : 1; }
+
 template <class R, bool RENORM>
 __global__ __launch_bounds__(256) void route_backward_kernel(
     const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
@@ -450,7 +448,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(
     const int32_t *__restrict__ tokens, float alpha, const float *__restrict__ d_loss,
     const int32_t *__restrict__ off, const uint8_t *__restrict__ mask, int T, int E, int k, int S,
     int C, float *__restrict__ out) {
-  constexpr int U = R::V <= 4 ? 4 : (R::V <= 8 ? 2 : 1), L = R::L, nq = kWave / L, NW = 256 / kWave;
+  constexpr int U = backward_batch<R>(), L = R::L, nq = kWave / L, NW = 256 / kWave;
   constexpr int step = NW * nq;
   using P = Picked<R, RENORM>;
   __shared__ __align__(16) float s_g[NW][U * kWave * R::V];
@@ -615,24 +613,19 @@ void with_row(int E, F f) {
   }
 }
 
-// token slots of a workgroup of the loss's first launch times tokens in flight
-int loss_batch(int E) {
-  int n = 0;
-  with_row(E, [&](auto row) {
-    using R = decltype(row);
-    n = unroll_of<R>() * kWavesP * (kWave / R::L);
-  });
-  return n;
-}
+// token slots of a workgroup of the loss's first launch
+int loss_batch(int E) { return kWavesP * (kWave / lanes_for(E)); }
 
 // Tokens per block of the loss's first launch.  A small batch is one block
 // (a workgroup's loads of a few thousand values cost less than a second
-// launch); otherwise one batch of the workgroup's token slots (the most that
-// is in flight at once), halved down to 16 while there are fewer than 512
-// blocks (two per CU).
+// launch); otherwise one batch of the workgroup's token slots, at least 64
+// tokens (the second launch reads as many slots as there are blocks: with 32
+// it takes 6.3 us instead of 5.1 at 32749 tokens of 256 experts, the first as
+// long as before), halved down to 16 while there are fewer than 512 blocks
+// (two per CU; with one, of 128 tokens, the first takes 22.6 us instead of 16).
 int loss_block(int T, int E, int S, int batch) {
   if (S == 1 && (long long)T * E <= 16384) return T > 0 ? T : 1;
-  int C = batch > 16 ? batch : 16;
+  int C = batch > 64 ? batch : 64;
   while (C > 16 && (T + C - 1) / C < 512) C >>= 1;
   return C;
 }
@@ -689,8 +682,8 @@ hipError_t launch_route_backward(const float *logits, const int32_t *topk_idx, c
                                  hipStream_t s) {
   with_row(E, [&](auto row) {
     using R = decltype(row);
-    // tokens per workgroup: one batch of its token slots, at least 16
-    const int C = max(16, (R::V <= 4 ? 4 : 2) * (256 / R::L));
+    // tokens per workgroup: one batch of its token slots, at least 8
+    const int C = max(8, backward_batch<R>() * (256 / R::L));
     const dim3 grid((T + C - 1) / C), block(256);
     if (renorm)
       hipLaunchKernelGGL((route_backward_kernel<R, true>), grid, block, 0, s, logits, topk_idx, dw,
