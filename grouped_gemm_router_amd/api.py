@@ -370,14 +370,14 @@ def moe_quantize_fp8(src, q, scale, *, block_rows=128, block_cols=128, stream=No
 # its type, shape, contiguity and device before the library is called.
 # ----------------------------------------------------------------------------
 
-def _arg(t, name, dtype, *shape, device):
+def _arg(t, name, dtype, shape, device):
     """Pointer of tensor t (None: NULL), which must be a contiguous
     dtype[shape] on the GPU `device` (an index)."""
     if t is None:
         return None
     try:
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.get_device() == device):
+        if (t.shape == shape and t.dtype is dtype and t.get_device() == device
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -385,7 +385,7 @@ def _arg(t, name, dtype, *shape, device):
         raise TypeError("%s must be a torch.Tensor, got %r" % (name, type(t)))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
+    if tuple(t.shape) != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -410,7 +410,7 @@ def _gpu(t, name):
     device = t.get_device()
     if device < 0:
         raise ValueError("%s must be on a GPU" % name)
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():  # (a GPU tensor is there: CUDA is initialised)
         raise ValueError("%s is on GPU %d, which is not the current device" % (name, device))
     return device
 
@@ -447,14 +447,16 @@ def _workspace(ws, size, device, stream):
 
 def _tokens(seq_offsets, token_mask, T, device):
     """(S, pointer of seq_offsets, pointer of token_mask)"""
+    if seq_offsets is None and token_mask is None:
+        return 1, None, None
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     if S < 1:
         raise ValueError("seq_offsets must hold at least two entries")
-    off = _arg(seq_offsets, "seq_offsets", torch.int32, S + 1, device=device)
+    off = _arg(seq_offsets, "seq_offsets", torch.int32, (S + 1,), device)
     mdt = torch.bool if token_mask is None else token_mask.dtype
     if mdt not in (torch.bool, torch.uint8):
         raise TypeError("token_mask must be bool or uint8, got %s" % mdt)
-    return S, off, _arg(token_mask, "token_mask", mdt, T, device=device)
+    return S, off, _arg(token_mask, "token_mask", mdt, (T,), device)
 
 
 def moe_balance_loss_workspace_size(T: int, E: int, S: int) -> int:
@@ -477,12 +479,12 @@ def moe_balance_loss(logits, topk_idx, counts, probs, tokens, loss, *, alpha=0.0
     i32, f32 = torch.int32, torch.float32
     ws, ws_bytes = _workspace(ws, moe_balance_loss_workspace_size(T, E, S), dev, stream)
     return _invoke("moe_balance_loss", lib.moe_balance_loss,
-                   _arg(logits, "logits", f32, T, E, device=dev),
-                   _arg(topk_idx, "topk_idx", i32, T, k, device=dev), off, mask, T, E, k, S,
-                   float(alpha), _arg(counts, "counts", i32, S, E, device=dev),
-                   _arg(probs, "probs", f32, S, E, device=dev),
-                   _arg(tokens, "tokens", i32, S + 1, device=dev),
-                   _arg(loss, "loss", f32, 1, device=dev), ws.data_ptr(), ws_bytes,
+                   _arg(logits, "logits", f32, (T, E), dev),
+                   _arg(topk_idx, "topk_idx", i32, (T, k), dev), off, mask, T, E, k, S,
+                   float(alpha), _arg(counts, "counts", i32, (S, E), dev),
+                   _arg(probs, "probs", f32, (S, E), dev),
+                   _arg(tokens, "tokens", i32, (S + 1,), dev),
+                   _arg(loss, "loss", f32, (1,), dev), ws.data_ptr(), ws_bytes,
                    _raw_stream(stream, dev))
 
 
@@ -499,13 +501,13 @@ def moe_route_backward(logits, topk_idx, d_logits, *, d_topk_w=None, flags=0, co
     S, off, mask = _tokens(seq_offsets, token_mask, T, dev)
     i32, f32 = torch.int32, torch.float32
     return _invoke("moe_route_backward", lib.moe_route_backward,
-                   _arg(logits, "logits", f32, T, E, device=dev),
-                   _arg(topk_idx, "topk_idx", i32, T, k, device=dev),
-                   _arg(d_topk_w, "d_topk_w", f32, T, k, device=dev), flags,
-                   _arg(counts, "counts", i32, S, E, device=dev),
-                   _arg(tokens, "tokens", i32, S + 1, device=dev), float(alpha),
-                   _arg(d_loss, "d_loss", f32, 1, device=dev), off, mask, T, E, k, S,
-                   _arg(d_logits, "d_logits", f32, T, E, device=dev), _raw_stream(stream, dev))
+                   _arg(logits, "logits", f32, (T, E), dev),
+                   _arg(topk_idx, "topk_idx", i32, (T, k), dev),
+                   _arg(d_topk_w, "d_topk_w", f32, (T, k), dev), flags,
+                   _arg(counts, "counts", i32, (S, E), dev),
+                   _arg(tokens, "tokens", i32, (S + 1,), dev), float(alpha),
+                   _arg(d_loss, "d_loss", f32, (1,), dev), off, mask, T, E, k, S,
+                   _arg(d_logits, "d_logits", f32, (T, E), dev), _raw_stream(stream, dev))
 
 
 def _lora_dt(dtype) -> int:
@@ -537,12 +539,12 @@ def moe_lora_linear(x, A, B, scale, adapter, y, v, *, W=None, ws=None, stream=No
     ws, ws_bytes = _workspace(ws, moe_lora_linear_workspace_size(T, N, K, r, n, dt), dev, stream)
     pw, ldw = _pitched(W, "W", dt, N, K, dev)
     return _invoke("moe_lora_linear", lib.moe_lora_linear,
-                   _arg(x, "x", dt, T, K, device=dev), pw, ldw,
-                   _arg(A, "A", dt, n, r, K, device=dev), _arg(B, "B", dt, n, r, N, device=dev),
-                   _lora_dt(dt), _arg(scale, "scale", f32, n, device=dev),
-                   _arg(adapter, "adapter", torch.int32, T, device=dev), T, N, K, r, n,
-                   _arg(y, "y", y.dtype, T, N, device=dev), _lora_dt(y.dtype),
-                   _arg(v, "v", f32, T, r, device=dev), ws.data_ptr(), ws_bytes, _raw_stream(stream, dev))
+                   _arg(x, "x", dt, (T, K), dev), pw, ldw,
+                   _arg(A, "A", dt, (n, r, K), dev), _arg(B, "B", dt, (n, r, N), dev),
+                   _lora_dt(dt), _arg(scale, "scale", f32, (n,), dev),
+                   _arg(adapter, "adapter", torch.int32, (T,), dev), T, N, K, r, n,
+                   _arg(y, "y", y.dtype, (T, N), dev), _lora_dt(y.dtype),
+                   _arg(v, "v", f32, (T, r), dev), ws.data_ptr(), ws_bytes, _raw_stream(stream, dev))
 
 
 def moe_lora_backward_workspace_size(T: int, N: int, K: int, r: int, n: int, dtype) -> int:
@@ -564,13 +566,13 @@ def moe_lora_linear_backward(dy, x, A, B, scale, adapter, v, u, *, W_t=None, dx=
     ws, ws_bytes = _workspace(ws, moe_lora_backward_workspace_size(T, N, K, r, n, dt), dev, stream)
     pw, ldw = _pitched(W_t, "W_t", dt, K, N, dev)
     return _invoke("moe_lora_linear_backward", lib.moe_lora_linear_backward,
-                   _arg(dy, "dy", dt, T, N, device=dev), _arg(x, "x", dt, T, K, device=dev), pw,
-                   ldw, _arg(A, "A", dt, n, r, K, device=dev),
-                   _arg(B, "B", dt, n, r, N, device=dev), _lora_dt(dt),
-                   _arg(scale, "scale", f32, n, device=dev),
-                   _arg(adapter, "adapter", torch.int32, T, device=dev),
-                   _arg(v, "v", f32, T, r, device=dev), T, N, K, r, n,
-                   _arg(u, "u", f32, T, r, device=dev), _arg(dx, "dx", dt, T, K, device=dev),
-                   _arg(dA, "dA", f32, n, r, K, device=dev),
-                   _arg(dB, "dB", f32, n, r, N, device=dev), ws.data_ptr(), ws_bytes,
+                   _arg(dy, "dy", dt, (T, N), dev), _arg(x, "x", dt, (T, K), dev), pw,
+                   ldw, _arg(A, "A", dt, (n, r, K), dev),
+                   _arg(B, "B", dt, (n, r, N), dev), _lora_dt(dt),
+                   _arg(scale, "scale", f32, (n,), dev),
+                   _arg(adapter, "adapter", torch.int32, (T,), dev),
+                   _arg(v, "v", f32, (T, r), dev), T, N, K, r, n,
+                   _arg(u, "u", f32, (T, r), dev), _arg(dx, "dx", dt, (T, K), dev),
+                   _arg(dA, "dA", f32, (n, r, K), dev),
+                   _arg(dB, "dB", f32, (n, r, N), dev), ws.data_ptr(), ws_bytes,
                    _raw_stream(stream, dev))
