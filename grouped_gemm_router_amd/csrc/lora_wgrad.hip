@@ -3,8 +3,9 @@
 //   dB[a][j] = sum over its rows t of v[t][j] dy[t].
 //
 // The rows are read in the plan's order, adapter by adapter, and each
-// adapter's rows are cut into units of at most TS.  A workgroup takes a unit, 128 columns and 16 or 32 ranks, and its
-// four waves take 32 rows in turn.  The sum runs over rows, so a lane loads
+// adapter's rows are cut into units of at most TS.  A workgroup takes a unit,
+// 128 columns and 16 or 32 ranks, and its four waves take 32 rows in turn (a
+// short unit's take 128 columns each).  The sum runs over rows, so a lane loads
 // 16 bytes (8 columns) of 8 rows and turns that 8 x 8 block in registers into
 // eight matrix-core fragments; x and dy are read once, in whole lines, which
 // is what bounds this (2 r flops per 2 bytes).  u and v are fp32 and enter as
@@ -18,6 +19,11 @@ namespace {
 using namespace moe;
 
 constexpr int kColTile = 128;
+// Rows of a unit up to which a workgroup's waves take 128 columns each and all
+// of the unit's rows, instead of 128 columns together and 32 rows in turn: most
+// of the waves would have none (777 rows of 33 adapters of rank 32, 9216
+// columns: 23.2 us, so 15.6).
+constexpr int kShortUnit = 64;
 
 // the slices behind the plan: an adapter of c > TS rows has fewer than
 // 2 c / TS units
@@ -37,12 +43,15 @@ __global__ __launch_bounds__(256) void wgrad_kernel(
   if ((int)blockIdx.x >= *n_units) return;
   const LoraUnit un = units[blockIdx.x];
   const int ka = (K + kColTile - 1) / kColTile;
-  const bool is_a = (int)blockIdx.y < ka;
-  const int C = is_a ? K : N, c0 = (is_a ? blockIdx.y : blockIdx.y - ka) * kColTile;
+  const bool is_a = (int)blockIdx.y < ka, cut = un.count > kShortUnit;
+  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+  const int ct = is_a ? blockIdx.y : blockIdx.y - ka;
+  if (!cut && ct % 4 != 0) return;
+  const int C = is_a ? K : N, c0 = (cut ? ct : ct + wv) * kColTile;
+  if (!cut && c0 >= C) return;
   const int j0 = blockIdx.z * 16 * NR;
   const char *q = is_a ? x : dy;
   const float *p = is_a ? u : v;
-  const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int fr = lane & 15, fq = lane >> 4;
   const int col = min(c0 + 8 * fr, C - 8);  // C is a multiple of 8
   f32x4 acc[NR][8];
@@ -51,7 +60,7 @@ __global__ __launch_bounds__(256) void wgrad_kernel(
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[b][f] = f32x4{};
 
-  for (int s = wv * 32; s < un.count; s += 4 * 32) {
+  for (int s = cut ? wv * 32 : 0; s < un.count; s += cut ? 4 * 32 : 32) {
     // rows past the unit's end load the last one and count as zero in both
     // operands (no load is under a condition: the loads are in flight
     // together); columns past C and ranks past r load the last ones and are
@@ -109,10 +118,23 @@ __global__ __launch_bounds__(256) void wgrad_kernel(
                 pv[b][i], __uint_as_float(qv[i][f >> 2 & (ES / 2 - 1)][f & 3]), acc[b][f], 0, 0, 0);
     }
   }
-  // the four waves' sums, in wave order
   const int width = un.slot < 0 ? C : K + N;
   float *out = un.slot < 0 ? (is_a ? dA : dB) + (size_t)un.adapter * r * C + c0
                            : part + (size_t)un.slot * r * width + (is_a ? c0 : K + c0);
+  if (!cut) {
+#pragma unroll
+    for (int b = 0; b < NR; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + b * 16 + 4 * fq + i;
+        if (j >= r || c0 + 8 * fr >= C) continue;
+        f32x4 *const to = reinterpret_cast<f32x4 *>(out + (size_t)j * width + 8 * fr);
+        to[0] = f32x4{acc[b][0][i], acc[b][1][i], acc[b][2][i], acc[b][3][i]};
+        to[1] = f32x4{acc[b][4][i], acc[b][5][i], acc[b][6][i], acc[b][7][i]};
+      }
+    return;
+  }
+  // the four waves' sums, in wave order
 #pragma unroll
   for (int b = 0; b < NR; ++b) {
     __syncthreads();
