@@ -81,7 +81,9 @@ __device__ __forceinline__ void st8(char *p, size_t i, int have, const float (&f
 }
 
 // Adapters among 32 rows up to which they go through the matrix cores one
-// after the other.
+// after the other.  1024 rows of N and K 4096 with a limit of 2, 6 and 8: rank
+// 16 of 100 adapters (4 a block) 63.1, 62.4, 62.3 us, of 160 65.1, 67.4, 67.1,
+// of 250 67.8, 70.5, 74.0; rank 64 of 160 125, 117, 114.
 constexpr int kBlockKinds = 6;
 
 // The adapters of a tile's row blocks.  count: how many a block of 32 rows
@@ -140,9 +142,9 @@ __device__ __forceinline__ void find_kinds(TileKinds &tk, const int *s_ad, int b
 // columns) are staged in LDS as the matrix cores' fragments, up to RC ranks of
 // all the tile's adapters at once.  What counts here is the number of
 // instructions: the code runs once a tile, from beyond the instruction cache,
-// where it arrives at some 50 ns per 64 bytes (measured).  Fragments built from
-// single elements took 9 us a tile for 16 ranks on 256 x 256, and for 32 ranks
-// of 2 to 3 adapters a block on 128 x 128.
+// where it arrives at some 50 ns per 64 bytes.  Measured per tile: 16 ranks of
+// one adapter on 256 x 256 6.6 us, with fragments built from single elements
+// 9.2; 32 ranks of 2 to 3 adapters a block on 128 x 128 6.9 us, so built 9.2.
 //
 // v_of(row): 256 bytes for a row of the tile; slab_of(i), i < NSLAB: SLAB
 // bytes each.  s_row, s_ad: the tile's rows and adapters (-1 for none).
@@ -347,103 +349,70 @@ __device__ __forceinline__ void load_row(int *s_row, int *s_ad, int i, int m0, c
 
 // rows [32 blk, 32 blk + 32) of a tile, staged in fp32 with row pitch SP, for
 // WM row blocks at once (stage_of(w) holds tile row block first + w * stride):
-// add what is left of the low-rank part and of y, round, store 8-column pieces
+// add what is left of the low-rank part (blocks without `done`) and of y,
+// round, store 8-column pieces.  The rows' own factors are what bounds a block
+// of many adapters: 64 rows of 64 adapters of 16 ranks, 128 columns, are 256 KB
+// a tile, in 9 us (two pieces a thread at once: the same).
 template <int ES, int OS, int BN, int SP, int WM, bool VEC, class StageOf>
-__device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int stride, int m0,
-                                              int n0, const int *s_row, const int *s_ad, const int *s_hom,
-                                            bool add_y,
-                                              const char *F, const float *v, int T, int N, int r,
-                                              char *y) {
-  constexpr int CG = BN / 8, P = 1;  // pieces that a thread has in hand at once
-  const int nt = blockDim.x;
-  for (int q0 = threadIdx.x; q0 < WM * 32 * CG; q0 += P * nt) {
-    float f[P][8];
-    bool live[P], low[P];
-    int have[P];
-    size_t at[P];
-    const float *vr[P];
-    const char *Fp[P];
+__device__ __forceinline__ void finish_pieces(StageOf stage_of, int first, int stride, int m0, int n0,
+                                              const int *s_row, const int *s_ad, const int *done,
+                                              bool add_y, const char *F, const float *v, int T, int N,
+                                              int r, char *y) {
+  constexpr int CG = BN / 8;
+  for (int q = threadIdx.x; q < WM * 32 * CG; q += blockDim.x) {
+    const int w = q / (32 * CG), rr = (q / CG) % 32, c = (q % CG) * 8;
+    const int blk = first + w * stride, row = blk * 32 + rr, col = n0 + c;
+    if (m0 + row >= T || col >= N) continue;
+    const int t = s_row[row], a = s_ad[row], have = N - col;
+    const float *st = stage_of(w) + rr * SP + c;
+    float f[8];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int q = min(q0 + p * nt, WM * 32 * CG - 1);
-      const int w = q / (32 * CG), rr = (q / CG) % 32, c = (q % CG) * 8;
-      const int blk = first + w * stride, row = blk * 32 + rr, col = n0 + c;
-      live[p] = q0 + p * nt < WM * 32 * CG && m0 + row < T && col < N;
-      const int tc = s_row[row], cc = live[p] ? col : 0;  // addresses that exist
-      have[p] = N - cc;
-      at[p] = (size_t)tc * N + cc;
-      const int a = s_ad[row];
-      low[p] = live[p] && a >= 0 && !s_hom[blk];
-      vr[p] = v + (size_t)tc * r;
-      Fp[p] = F + ((size_t)max(a, 0) * r * N + cc) * ES;
-      const float *st = stage_of(w) + rr * SP + c;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[p][i] = st[i];
-    }
-    if (low[0] || low[P - 1]) {
-      // 16 ranks a step, all loads of a step before its first product; a
-      // piece without a low-rank part loads an adapter's rows and drops them
-      float g[P][8];
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[p][i] = f[p][i];
+    for (int i = 0; i < 8; ++i) f[i] = st[i];
+    if (a >= 0 && !done[blk]) {
+      const float *const vr = v + (size_t)t * r;
+      const char *const Fa = F + ((size_t)a * r * N + col) * ES;
+      // 16 ranks a step, all loads of a step before its first product
       for (int j0 = 0; j0 < r; j0 += 16) {
-        Raw8<ES, VEC> w[P][16];
-        f32x4 vv[P][4];
+        Raw8<ES, VEC> fv[16];
+        f32x4 vv[4];
         const int j8 = min(j0 + 8, r - 8);  // (r % 16 == 8: loaded again, not used)
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
+        for (int j = 0; j < 16; ++j) fv[j].load(Fa, (size_t)(j < 8 ? j0 + j : j8 + j - 8) * N, have);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[p][j].load(Fp[p], (size_t)(j < 8 ? j0 + j : j8 + j - 8) * N, have[p]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            vv[p][j] = *reinterpret_cast<const f32x4 *>(vr[p] + (j < 2 ? j0 : j8 - 8) + 4 * j);
-        }
+        for (int j = 0; j < 4; ++j)
+          vv[j] = *reinterpret_cast<const f32x4 *>(vr + (j < 2 ? j0 : j8 - 8) + 4 * j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && j0 + 8 >= r) break;
 #pragma unroll
-          for (int p = 0; p < P; ++p)
+          for (int j = 8 * h; j < 8 * h + 8; ++j)
 #pragma unroll
-            for (int j = 8 * h; j < 8 * h + 8; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                g[p][i] = fmaf(vv[p][j >> 2][j & 3], w[p][j].get(i), g[p][i]);
+            for (int i = 0; i < 8; ++i) f[i] = fmaf(vv[j >> 2][j & 3], fv[j].get(i), f[i]);
         }
       }
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[p][i] = low[p] ? g[p][i] : f[p][i];
     }
+    const size_t at = (size_t)t * N + col;
+    if (add_y) {
+      Raw8<OS, VEC> old;
+      old.load(y, at, have);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (!live[p]) continue;
-      if (add_y) {
-        Raw8<OS, VEC> old;
-        old.load(y, at[p], have[p]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[p][i] += old.get(i);
-      }
-      st8<OS, VEC>(y, at[p], have[p], f[p]);
+      for (int i = 0; i < 8; ++i) f[i] += old.get(i);
     }
+    st8<OS, VEC>(y, at, have, f);
   }
 }
 
 template <int ES, int OS, int BN, int SP, int WM, class StageOf>
 __device__ __forceinline__ void finish_rows(StageOf stage_of, int first, int stride, int m0, int n0,
-                                            const int *s_row, const int *s_ad, const int *s_hom,
-                                            bool add_y,
-                                            const char *F, const float *v, int T, int N, int r,
-                                            char *y) {
+                                            const int *s_row, const int *s_ad, const int *done,
+                                            bool add_y, const char *F, const float *v, int T, int N,
+                                            int r, char *y) {
   if (N % 8 == 0)  // rows of F and of y are then 16-byte aligned
-    finish_pieces<ES, OS, BN, SP, WM, true>(stage_of, first, stride, m0, n0, s_row, s_ad, s_hom, add_y, F, v,
-                                            T, N, r, y);
+    finish_pieces<ES, OS, BN, SP, WM, true>(stage_of, first, stride, m0, n0, s_row, s_ad, done, add_y,
+                                            F, v, T, N, r, y);
   else
-    finish_pieces<ES, OS, BN, SP, WM, false>(stage_of, first, stride, m0, n0, s_row, s_ad, s_hom, add_y, F,
-                                             v, T, N, r, y);
+    finish_pieces<ES, OS, BN, SP, WM, false>(stage_of, first, stride, m0, n0, s_row, s_ad, done, add_y,
+                                             F, v, T, N, r, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -475,14 +444,14 @@ __global__ __launch_bounds__(kF32Threads) void expand_f32_kernel(
   constexpr int BM = 64, BNF = 64, SP = BNF + 4, ROWS = BM + BNF, NLD = 2 * ROWS * 8 / kF32Threads;
   __shared__ u32x4 ring[2][2][ROWS * 8];  // step parity, group
   __shared__ int s_row[BM], s_ad[BM];
-  __shared__ int s_hom[BM / 32];
+  __shared__ int s_done[BM / 32];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
   const int m0 = at.mt * BM, n0 = at.nt * BNF;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int grp = wv / 4, wm = wv / 2 % 2, wn = wv % 2, fr = lane & 31, fh = lane >> 5;
   if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
-  if (tid < BM / 32) s_hom[tid] = 0;
+  if (tid < BM / 32) s_done[tid] = 0;
   f32x16 acc = f32x16{};
   __syncthreads();
   if (W) {
@@ -533,7 +502,7 @@ __global__ __launch_bounds__(kF32Threads) void expand_f32_kernel(
     __syncthreads();
   }
   finish_rows<4, 4, BNF, SP, 2>([&](int w) { return stage + w * 32 * SP; }, 0, 1, m0, n0, s_row,
-                                s_ad, s_hom, W == nullptr, F, v, T, N, r, y);
+                                s_ad, s_done, W == nullptr, F, v, T, N, r, y);
 }
 
 // Tiles of 32 x 32 whose eight waves cut K, operands straight from memory:
@@ -548,14 +517,14 @@ __global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
   constexpr int BM = 32, BNF = 32, SP = BNF + 4;
   __shared__ float red[kF32Waves][BM * SP];
   __shared__ int s_row[BM], s_ad[BM];
-  __shared__ int s_hom[1];
+  __shared__ int s_done[1];
   const TileAt at = tile_at(blockIdx.x, MT, NT);
   if (at.mt < 0) return;
   const int m0 = at.mt * BM, n0 = at.nt * BNF;
   const int tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int fr = lane & 31, fh = lane >> 5;
   if (tid < BM) load_row(s_row, s_ad, tid, m0, adapter, order, T, n);
-  if (tid == 0) s_hom[0] = 0;
+  if (tid == 0) s_done[0] = 0;
   f32x16 acc = f32x16{};
   __syncthreads();
   if (W) {
@@ -599,14 +568,26 @@ __global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
     red[0][o] = sum;
   }
   __syncthreads();
-  finish_rows<4, 4, BNF, SP, 1>([&](int) { return &red[0][0]; }, 0, 1, m0, n0, s_row, s_ad, s_hom,
+  finish_rows<4, 4, BNF, SP, 1>([&](int) { return &red[0][0]; }, 0, 1, m0, n0, s_row, s_ad, s_done,
                                 W == nullptr, F, v, T, N, r, y);
 }
 
 // ---------------------------------------------------------------------------
 // bf16: tiles of BM x BN on 4 waves (WM x WN), operands by LDS-direct loads
-// through a ring of NS slots of one 64-deep K step each, one barrier a step.  The ring's slots are separate LDS arrays, so that the
-// compiler does not wait for a load into one slot before it reads another.
+// through a ring of four slots of one 64-deep K step each, one barrier a step.
+// The ring's slots are separate LDS arrays, so that the compiler does not wait
+// for a load into one slot before it reads another.  What bounds it is the
+// rate at which a CU takes in operands: 50 to 60 bytes a ns whatever the shape
+// (1331 rows, N 2048, K 7168 on 128 x 128: 50 us for 112 steps of 32 KB on 176
+// CUs, the matrix cores busy 46 % of it; 128 rows, N 14336, K 4096: W streams
+// at 4 TB/s).
+//
+// rot: workgroups of different columns begin at different K, so that their
+// loads of W do not all hit the same memory channels (W's rows are a power of
+// two apart): 128 rows of 4096 x 14336 36.2 us instead of 38.6.  With more
+// rows the tiles that share x want the same part of it at the same time: 512
+// rows 36.3 us instead of 29.6.
+//
 // Pieces past K come from a zero in memory (the last steps only); rows past T
 // and columns past N repeat the last one and are not stored.
 // ---------------------------------------------------------------------------

@@ -88,10 +88,13 @@ inline LoraPlan lora_plan(int T, int N, int K, int r, int n, int es, bool backwa
 }
 
 // Whether the forward pass reads its rows through a plan: not where reading
-// every row's factors (the most that unsorted rows can cost, at some 5 bytes
-// a ps) takes less than the plan's launch and the longer way through it.
+// every row's factors, the most that rows in any order can cost, takes less
+// than the plan's launch and the longer way through it.  Measured in order /
+// through a plan, us: 128 rows of N 14336, K 4096 (75e6 bytes) 48 / 55; N and
+// K 4096: 512 rows of rank 16 (134e6) 39 / 44 on 64 adapters, 37 / 40 on 8;
+// 1024 rows (268e6) 65 / 62 on 100 adapters, 66 / 67 on 160.
 inline bool lora_sorts(int T, int N, int K, int r, int es) {
-  return (double)T * r * ((double)N + K) * es > 128e6;
+  return (double)T * r * ((double)N + K) * es > 250e6;
 }
 
 hipError_t launch_lora_plan(const int32_t *adapter, int T, int n, const LoraPlan &p, bool units,

@@ -79,8 +79,8 @@ def test_lora_linear_validation(lib):
                 dict(dt=F32), dict(T=(1 << 24) + 1), dict(N=(1 << 20) + 1),
                 dict(T=1 << 24, N=1 << 13)):
         assert f(**bad) == UNSUPPORTED, bad
-    big = dict(T=1000, N=4096, K=4096)
-    need = lib.moe_lora_linear_workspace_size(1000, 4096, 4096, 8, 2, BF16)
+    big = dict(T=4000, N=4096, K=4096)
+    need = lib.moe_lora_linear_workspace_size(4000, 4096, 4096, 8, 2, BF16)
     assert need > 0 and f(**big, ws=P, wsb=need - 1) == WORKSPACE
     assert f(**big, ws=MIS, wsb=need) == INVALID
 

@@ -502,8 +502,9 @@ def test_refusals_on_the_gpu():
 # than are staged at once, tiles of every size
 @pytest.mark.parametrize("out_dt", [BF, F32])
 @pytest.mark.parametrize("T,N,K,r,n", [
-    (600, 1000, 512, 72, 40), (700, 1200, 256, 128, 12), (1500, 1111, 256, 64, 100),
-    (2100, 3000, 256, 40, 200), (5000, 4096, 128, 128, 400), (300, 2050, 1024, 128, 30)])
+    (600, 1000, 2048, 72, 40), (700, 1200, 256, 128, 12), (1500, 1111, 256, 64, 100),
+    (2100, 3000, 256, 40, 200), (5000, 4096, 128, 128, 400), (330, 2050, 1024, 128, 30),
+    (6000, 2048, 256, 16, 5), (4100, 1600, 640, 24, 900), (8000, 1500, 512, 8, 300)])
 def test_blocks_of_a_few_adapters(T, N, K, r, n, out_dt):
     print("lora few", T, N, K, r, n, out_dt, flush=True)
     c = Case(T, N, K, r, n, BF, "mixed", T).gpu()
@@ -524,7 +525,7 @@ def test_adapted_linear_graph_beside_larger_calls():
     nothing of it, nor it of them."""
     from grouped_gemm_router_amd.adapters import AdaptedLinear
     small = [Case(200, 512, 2048, 32, 9, BF, "mixed", i).gpu() for i in range(4)]
-    large = Case(1500, 512, 2048, 32, 9, BF, "mixed", 9).gpu()
+    large = Case(1600, 512, 2048, 32, 9, BF, "mixed", 9).gpu()
     s0 = small[0]
     lin = AdaptedLinear(s0.g_W, s0.g_A, s0.g_B, s0.g_scale, grad=True)
 
