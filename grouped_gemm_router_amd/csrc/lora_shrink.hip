@@ -231,33 +231,31 @@ __global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
   }
 }
 
-// The tiles' slices added in slice order.  A launch of its own: a flag between
-// workgroups of the same launch needs their XCDs' L2 written back, which took
-// five times as long as the products.  grid (4 parts of a tile's rows times
-// tiles, rank groups)
+// The slices of the sums added in slice order, four ranks of a row a thread.
+// A launch of its own: a flag between workgroups of the same launch needs
+// their XCDs' L2 written back, which took five times as long as the products.
+// grid (pieces of T RP, rank groups).  Rows without an adapter have their
+// zeros already.
 __global__ __launch_bounds__(256) void shrink_sum_kernel(
     const float *__restrict__ part, const float *__restrict__ scale,
-    const int32_t *__restrict__ order, const int32_t *__restrict__ starts,
-    const int32_t *__restrict__ tiles, int T, int slices, int RP, int r, int n,
-    float *__restrict__ v) {
-  const int tile = blockIdx.x / 4, j0 = blockIdx.y * RP;
-  if (tile >= tiles[n + 1]) return;
-  const TileRows tr = tile_rows(starts, tiles, n, tile);
-  if (tr.a == n) return;
-  const float *all = part + ((size_t)blockIdx.y * slices * T + tr.first) * RP;
-  const int r0 = (blockIdx.x % 4) * (kShrinkTile / 4);
-  for (int i = threadIdx.x; i < kShrinkTile / 4 * RP; i += 256) {
-    const int row = r0 + i / RP, j = i % RP;
-    if (row >= tr.rows || j0 + j >= r) continue;
-    float p[kShrinkSlices];
+    const int32_t *__restrict__ adapter, const int32_t *__restrict__ order, int T, int slices, int RP,
+    int r, int n, float *__restrict__ v) {
+  const int i = blockIdx.x * 256 + threadIdx.x, row = i / (RP / 4), jr = i % (RP / 4) * 4,
+            j = blockIdx.y * RP + jr;
+  if (row >= T || j >= r) return;
+  const float *const all = part + ((size_t)blockIdx.y * slices * T + row) * RP + jr;
+  f32x4 p[kShrinkSlices];
 #pragma unroll
-    for (int k = 0; k < kShrinkSlices; ++k)
-      p[k] = all[((size_t)min(k, slices - 1) * T + row) * RP + j];
-    float sum = p[0];
+  for (int k = 0; k < kShrinkSlices; ++k)
+    p[k] = *reinterpret_cast<const f32x4 *>(all + (size_t)min(k, slices - 1) * T * RP);
+  const int t = order[row], a = adapter[t];
+  if (a < 0 || a >= n) return;
+  f32x4 sum = p[0];
 #pragma unroll
-    for (int k = 1; k < kShrinkSlices; ++k) sum += k < slices ? p[k] : 0.f;
-    v[(size_t)order[tr.first + row] * r + j0 + j] = scale[tr.a] * sum;
-  }
+  for (int k = 1; k < kShrinkSlices; ++k)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum[c] += k < slices ? p[k][c] : 0.f;
+  *reinterpret_cast<f32x4 *>(v + (size_t)t * r + j) = scale[a] * sum;
 }
 
 template <int ES>
@@ -284,8 +282,8 @@ void launch_t(const void *x, const void *F, const float *scale, const int32_t *a
   else MOE_SHRINK(4);
 #undef MOE_SHRINK
   if (slices > 1)
-    hipLaunchKernelGGL(shrink_sum_kernel, dim3((unsigned)p->max_tiles * 4, groups), dim3(256), 0, s,
-                       part, scale, order, starts, tiles, T, slices, 16 * NR, r, n, v);
+    hipLaunchKernelGGL(shrink_sum_kernel, dim3((unsigned)(((size_t)T * 4 * NR + 255) / 256), groups),
+                       dim3(256), 0, s, part, scale, adapter, order, T, slices, 16 * NR, r, n, v);
 }
 
 }  // namespace
