@@ -156,7 +156,8 @@ __device__ __forceinline__ void shrink_slice(const char *x, const char *F, const
       for (int i = 0; i < 4; ++i) red[b * 16 + 4 * fq + i][q * 16 + fr] = acc[b][q][i];
 }
 
-// A tile's adapter (n: none), first place in the order and number of rows.
+// A tile's adapter (n: none, n + 1: no such tile), first place in the order and
+// number of rows.
 // tiles[a]: the adapters' first tiles (tiles[n]: of the rows without an
 // adapter, tiles[n + 1]: all); starts[a]: their first rows in the order.  The
 // adapter a with tiles[a] <= tile < tiles[a + 1] is found 64 probes at a time.
@@ -179,6 +180,7 @@ __device__ __forceinline__ TileRows tile_rows(const int32_t *starts, const int32
     lo += f * step;
     cnt = hit - lo;
   }
+  if (lo > n) return {lo, 0, 0};
   const int first = starts[lo] + (tile - tiles[lo]) * kShrinkTile;
   return {lo, first, min(starts[lo + 1] - first, kShrinkTile)};
 }
@@ -195,9 +197,9 @@ __global__ __launch_bounds__(kTileThreads) void shrink_tile_kernel(
   __shared__ int s_row[kShrinkTile];
   const int tid = threadIdx.x, wv = tid / kWave;
   const int tile = blockIdx.x / slices, ks = blockIdx.x % slices, j0 = blockIdx.y * RP;
-  if (tile >= tiles[n + 1]) return;
   const TileRows tr = tile_rows(starts, tiles, n, tile);
   const int a = tr.a, rows = tr.rows;
+  if (a > n) return;
   if (a == n) {  // rows without an adapter
     if (ks == 0)
       for (int i = tid; i < rows * RP; i += kTileThreads) {
