@@ -437,9 +437,10 @@ def _workspace(ws, size, device, stream):
     if ws is None:
         if _deferring():
             raise ValueError("a call under deferred() needs its workspace passed")
-        ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda:%d" % device)
-        if stream is not None:
-            ws.record_stream(stream)
+        # from the memory of the call's own stream: a block that the current
+        # stream's pending work has only just let go would be written early
+        with torch.cuda.stream(stream):  # (None: the current stream)
+            ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda:%d" % device)
     elif not ws.is_contiguous() or ws.get_device() != device:
         raise ValueError("ws must be contiguous and on GPU %d" % device)
     return ws, ws.numel() * ws.element_size()

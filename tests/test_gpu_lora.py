@@ -575,3 +575,25 @@ def test_refuses_another_devices_stream():
     with pytest.raises(ValueError, match="stream"):
         a.moe_lora_linear(c.g_x, c.g_A, c.g_B, c.g_scale, c.g_adapter, y, v, W=c.g_W,
                           ws=torch.empty(16, dtype=torch.uint8, device=DEV), stream=Other())
+
+
+def test_workspace_comes_from_the_calls_stream():
+    """A workspace made for a call on a side stream is that stream's memory:
+    the current stream's may still be in use by work that is pending there."""
+    a = api()
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        ws, size = a._workspace(None, 3 << 20, 0, stream)
+        assert size == 3 << 20
+        owner = [seg["stream"] for seg in torch.cuda.memory_snapshot()
+                 if seg["address"] <= ws.data_ptr() < seg["address"] + seg["total_size"]]
+        want = torch.cuda.current_stream() if stream is None else stream
+        assert owner == [want.cuda_stream]
+    # and such a call gives what the current stream's gives
+    c = Case(1600, 512, 2048, 32, 9, BF, "mixed", 1).gpu()
+    y0, v0 = forward(c, BF)
+    y1, v1 = torch.empty_like(y0), torch.empty_like(v0)
+    side.wait_stream(torch.cuda.current_stream())
+    a.moe_lora_linear(c.g_x, c.g_A, c.g_B, c.g_scale, c.g_adapter, y1, v1, W=c.g_W, stream=side)
+    side.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(v0, v1)
