@@ -157,9 +157,9 @@ __device__ __forceinline__ void shrink_slice(const char *x, const char *F, const
 }
 
 // A tile's adapter (n: none, n + 1: no such tile), first place in the order and
-// number of rows.  tiles[a]: the adapters' first tiles (tiles[n]: of the rows without an
-// adapter, tiles[n + 1]: all); starts[a]: their first rows in the order.  The
-// adapter a with tiles[a] <= tile < tiles[a + 1] is found 64 probes at a time.
+// number of rows.  tiles[a]: the adapters' first tiles (tiles[n]: of the rows
+// without an adapter, tiles[n + 1]: all); starts[a]: their first rows in the
+// order.  The adapter a with tiles[a] <= tile < tiles[a + 1] is found 64 probes at a time.
 // Must be called by whole waves.
 struct TileRows {
   int a, first, rows;

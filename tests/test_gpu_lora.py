@@ -140,9 +140,8 @@ def check_forward(c, out_dt, with_w=True, ldw_pad=0):
     return y, v
 
 
-# (T, N, K, r, n): row counts at every switch between the kernels (16, 32, 64
-# rows of the few-row kernel, 128 of the per-row shrink), column counts that
-# choose every tile shape, odd N, K that ends inside a 128-byte piece
+# (T, N, K, r, n): row counts at every switch between the kernels (16 and 32
+# rows of the few-row kernel), column counts that choose every tile shape, odd N, K that ends inside a 128-byte piece
 SIZES = [
     (1, 1, 8, 8, 1), (1, 256, 128, 8, 3), (1, 100, 4096, 16, 2), (2, 33, 72, 8, 2),
     (15, 64, 256, 16, 5), (16, 17, 200, 24, 16), (17, 130, 264, 32, 4), (32, 512, 512, 64, 3),
