@@ -205,7 +205,8 @@ class MoELayer:
         """Balance loss and per-expert counts of the last forward's routing
         (needs keep_logits): a dict of loss [1], counts [S][E], probs [S][E]
         and tokens [S+1] device tensors, over the sequences and the mask of
-        moe_balance_loss.  Enqueued on the current stream."""
+        moe_balance_loss, and the alpha, seq_offsets and token_mask that
+        route_backward() takes from it.  Enqueued on the current stream."""
         if self.logits is None:
             raise RuntimeError("balance_loss needs the logits: build the layer with "
                                "keep_logits=True")
@@ -214,27 +215,53 @@ class MoELayer:
         out = {"loss": torch.empty((1,), dtype=f32, device=dev),
                "counts": torch.empty((S, self.E), dtype=i32, device=dev),
                "probs": torch.empty((S, self.E), dtype=f32, device=dev),
-               "tokens": torch.empty((S + 1,), dtype=i32, device=dev)}
+               "tokens": torch.empty((S + 1,), dtype=i32, device=dev),
+               "alpha": alpha, "seq_offsets": seq_offsets, "token_mask": token_mask}
         api.moe_balance_loss(self.logits, self.topk_idx, out["counts"], out["probs"],
                              out["tokens"], out["loss"], alpha=alpha, seq_offsets=seq_offsets,
                              token_mask=token_mask)
         return out
 
-    def route_backward(self, d_topk_w=None, *, balance=None, d_loss=None, alpha: float = 0.01,
+    def route_backward(self, d_topk_w=None, *, balance=None, d_loss=None, alpha=None,
                        seq_offsets=None, token_mask=None):
         """Gradient [T][E] of the last forward's router logits: of its gate
-        weights from d_topk_w [T][k], and of a balance_loss() result (same
-        alpha, sequences and mask) from d_loss [1] (None: 1)."""
+        weights from d_topk_w [T][k], and of a balance_loss() result from
+        d_loss [1] (None: 1).  alpha, sequences and mask are the result's;
+        those given here must agree with them (of tensors only whether there
+        are any is checked).  Without a result, seq_offsets and token_mask say
+        which tokens take part."""
         if self.logits is None:
             raise RuntimeError("route_backward needs the logits: build the layer with "
                                "keep_logits=True")
+        if balance:
+            alpha = self._agreed(balance, "alpha", alpha)
+            seq_offsets = self._agreed(balance, "seq_offsets", seq_offsets)
+            token_mask = self._agreed(balance, "token_mask", token_mask)
         d_logits = torch.empty_like(self.logits)
         api.moe_route_backward(self.logits, self.topk_idx, d_logits, d_topk_w=d_topk_w,
                                flags=self.flags if d_topk_w is not None else 0,
                                counts=balance["counts"] if balance else None,
-                               tokens=balance["tokens"] if balance else None, alpha=alpha,
+                               tokens=balance["tokens"] if balance else None,
+                               alpha=0.01 if alpha is None else alpha,
                                d_loss=d_loss, seq_offsets=seq_offsets, token_mask=token_mask)
         return d_logits
+
+    @staticmethod
+    def _agreed(balance, name, given):
+        """What a balance_loss() result holds under name, or `given` where it
+        holds nothing (a dict of counts and tokens from elsewhere); a given
+        value that differs is refused."""
+        if name not in balance:
+            return given
+        kept = balance[name]
+        if given is None:
+            return kept
+        if isinstance(given, torch.Tensor) and isinstance(kept, torch.Tensor):
+            return given
+        if isinstance(given, torch.Tensor) or isinstance(kept, torch.Tensor) or given != kept:
+            raise ValueError("%s differs from the balance loss's: %r, there %r"
+                             % (name, given, kept))
+        return kept
 
     def capture(self, x, out):
         """A HIP graph (torch.cuda.CUDAGraph) of the five calls on x -> out,

@@ -1,0 +1,71 @@
+"""CPU checks of the layer's training methods and of the adapters' binding:
+what they pass on and what they refuse, with the library's calls recorded
+instead of made."""
+import pytest
+import torch
+
+from grouped_gemm_router_amd import api
+from grouped_gemm_router_amd.layer import MoELayer
+
+T, E, K = 6, 8, 2
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's training calls, recorded as (name, positional, keywords)."""
+    seen = []
+    for name in ("moe_balance_loss", "moe_route_backward"):
+        monkeypatch.setattr(api, name,
+                            lambda *a, _n=name, **k: seen.append((_n, a, k)))
+    return seen
+
+
+def layer():
+    """A layer after a forward pass, without weights."""
+    m = MoELayer.__new__(MoELayer)
+    m.E, m.k, m.flags, m.device = E, K, api.MOE_ROUTE_RENORM, torch.device("cpu")
+    m.logits = torch.zeros((T, E))
+    m.topk_idx = torch.zeros((T, K), dtype=torch.int32)
+    return m
+
+
+def test_the_gradient_takes_the_losss_alpha_sequences_and_mask(calls):
+    m = layer()
+    off = torch.tensor([0, 2, 5], dtype=torch.int32)
+    mask = torch.ones(T, dtype=torch.bool)
+    bal = m.balance_loss(0.25, seq_offsets=off, token_mask=mask)
+    dw = torch.zeros((T, K))
+    m.route_backward(dw, balance=bal)
+    m.route_backward(dw, balance=bal, alpha=0.25, seq_offsets=off.clone(), token_mask=mask.clone())
+    for name, _, kw in calls[1:]:
+        assert name == "moe_route_backward" and kw["alpha"] == 0.25
+        assert kw["counts"] is bal["counts"] and kw["tokens"] is bal["tokens"]
+        assert torch.equal(kw["seq_offsets"], off) and torch.equal(kw["token_mask"], mask)
+
+
+def test_a_gradient_that_disagrees_with_its_loss_is_refused(calls):
+    m = layer()
+    off = torch.tensor([0, T], dtype=torch.int32)
+    mask = torch.ones(T, dtype=torch.bool)
+    bal = m.balance_loss(0.25)
+    for bad in (dict(alpha=0.01), dict(seq_offsets=off), dict(token_mask=mask)):
+        with pytest.raises(ValueError, match=next(iter(bad))):
+            m.route_backward(balance=bal, **bad)
+    assert [c[0] for c in calls] == ["moe_balance_loss"]
+
+
+def test_a_gradient_without_the_layers_loss(calls):
+    """The gate's part alone, and counts and tokens from elsewhere: as given,
+    alpha 0.01 by default."""
+    m = layer()
+    mask = torch.ones(T, dtype=torch.bool)
+    m.route_backward(torch.zeros((T, K)), token_mask=mask)
+    own = {"counts": torch.zeros((1, E), dtype=torch.int32),
+           "tokens": torch.zeros(2, dtype=torch.int32)}
+    m.route_backward(balance=own, token_mask=mask)
+    m.route_backward(balance=own, alpha=0.5)
+    (_, _, a), (_, _, b), (_, _, c) = calls
+    assert a["alpha"] == b["alpha"] == 0.01 and c["alpha"] == 0.5
+    assert a["counts"] is None and b["counts"] is own["counts"]
+    assert a["token_mask"] is mask and b["token_mask"] is mask and c["token_mask"] is None
+    assert a["flags"] == api.MOE_ROUTE_RENORM and b["flags"] == 0
