@@ -48,12 +48,16 @@ class AdaptedLinear:
 
     def backward(self, dy, x, adapter, v):
         """(dx [T][K], dA [n][r][K], dB [n][r][N]) for the dy [T][N] of a
-        forward(x, adapter) that returned v; dA and dB are fp32."""
+        forward(x, adapter) that returned v; dA and dB are fp32.  dy and dx are
+        of the weights' type: the caller rounds the gradient of fp32 outputs
+        of bf16 weights."""
         if self.W_t is None:
             raise RuntimeError("backward needs W transposed: build with grad=True")
+        if dy.dtype != self.A.dtype:
+            raise TypeError("dy must be %s, the weights' type, got %s" % (self.A.dtype, dy.dtype))
         T, f32, dev = x.shape[0], torch.float32, x.device
         u = torch.empty((T, self.r), dtype=f32, device=dev)
-        dx = torch.empty((T, self.K), dtype=dy.dtype, device=dev)
+        dx = torch.empty((T, self.K), dtype=self.A.dtype, device=dev)
         dA = torch.empty((self.n, self.r, self.K), dtype=f32, device=dev)
         dB = torch.empty((self.n, self.r, self.N), dtype=f32, device=dev)
         api.moe_lora_linear_backward(dy, x, self.A, self.B, self.scale, adapter, v, u,

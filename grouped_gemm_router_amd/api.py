@@ -555,15 +555,18 @@ def moe_lora_backward_workspace_size(T: int, N: int, K: int, r: int, n: int, dty
 def moe_lora_linear_backward(dy, x, A, B, scale, adapter, v, u, *, W_t=None, dx=None, dA=None,
                              dB=None, ws=None, stream=None):
     """Gradients of moe_lora_linear with a frozen W: dy [T][N], x, A, B,
-    scale, adapter and v as in the forward pass; W_t [K][N] is W transposed.
+    scale, adapter and v as in the forward pass, dy of A's type; W_t [K][N] is
+    W transposed.
     Written: u [T][r] fp32, dx [T][K] (W_t None: the low-rank part is added to
     dx in place) and, if given, dA [n][r][K] and dB [n][r][N] fp32.  ws:
     moe_lora_backward_workspace_size bytes; when None, one is allocated here
     for this call."""
     T, N = dy.shape
     n, r, K = A.shape
-    dt, f32 = dy.dtype, torch.float32
+    dt, f32 = A.dtype, torch.float32
     dev = _gpu(dy, "dy")
+    if dy.dtype != dt:
+        raise TypeError("dy must be %s, like A, got %s" % (dt, dy.dtype))
     ws, ws_bytes = _workspace(ws, moe_lora_backward_workspace_size(T, N, K, r, n, dt), dev, stream)
     pw, ldw = _pitched(W_t, "W_t", dt, K, N, dev)
     return _invoke("moe_lora_linear_backward", lib.moe_lora_linear_backward,

@@ -69,3 +69,30 @@ def test_a_gradient_without_the_layers_loss(calls):
     assert a["counts"] is None and b["counts"] is own["counts"]
     assert a["token_mask"] is mask and b["token_mask"] is mask and c["token_mask"] is None
     assert a["flags"] == api.MOE_ROUTE_RENORM and b["flags"] == 0
+
+
+# ---------------------------------------------------------------------------
+# adapters
+# ---------------------------------------------------------------------------
+
+def adapted(N, grad, dt=torch.bfloat16):
+    from grouped_gemm_router_amd.adapters import AdaptedLinear
+    z = lambda *s: torch.zeros(s, dtype=dt)  # noqa: E731
+    return AdaptedLinear(z(N, 16), z(2, 8, 16), z(2, 8, N), torch.ones(2), grad=grad)
+
+
+def test_a_gradient_of_another_type_is_refused_by_its_name():
+    """An fp32 gradient of fp32 outputs of bf16 weights."""
+    lin = adapted(64, True)
+    x, a, v = torch.zeros((T, 16), dtype=torch.bfloat16), torch.zeros(T, dtype=torch.int32), None
+    with pytest.raises(TypeError, match="dy"):
+        lin.backward(torch.zeros((T, 64)), x, a, v)
+
+
+def test_the_binding_names_a_dy_of_another_type(monkeypatch):
+    monkeypatch.setattr(api, "_gpu", lambda t, name: 0)
+    z = torch.zeros
+    A, B = (z(2, 8, n, dtype=torch.bfloat16) for n in (16, 64))
+    with pytest.raises(TypeError, match="dy"):
+        api.moe_lora_linear_backward(z(T, 64), z(T, 16, dtype=torch.bfloat16), A, B, z(2),
+                                     z(T, dtype=torch.int32), z(T, 8), z(T, 8))
