@@ -18,7 +18,8 @@ from .layer import padded_weights
 class AdaptedLinear:
     """W [N][K] shared and frozen; A [n][r][K], B [n][r][N] the adapters'
     factors (rank-major; an adapter of a lower rank has zero rows behind it),
-    scale [n] fp32.  ``grad`` also keeps W transposed for the backward pass.
+    scale [n] fp32.  ``grad`` also keeps W transposed for the backward pass
+    and requires N % 8 == 0 (the forward pass takes any N).
     A and B are used as they are, so an optimiser may update them in place."""
 
     def __init__(self, W, A, B, scale, *, grad=False):
@@ -26,6 +27,8 @@ class AdaptedLinear:
         self.n, self.r, _ = A.shape
         assert A.shape == (self.n, self.r, self.K) and B.shape == (self.n, self.r, self.N)
         assert A.dtype == W.dtype and B.dtype == W.dtype
+        if grad and self.N % 8:
+            raise ValueError("grad=True requires N %% 8 == 0, got N = %d" % self.N)
         self.A, self.B, self.scale = A, B, scale
         # row pitch as for the expert weights
         self.W = padded_weights(W[None])[0]

@@ -81,6 +81,14 @@ def adapted(N, grad, dt=torch.bfloat16):
     return AdaptedLinear(z(N, 16), z(2, 8, 16), z(2, 8, N), torch.ones(2), grad=grad)
 
 
+def test_adapted_linear_refuses_a_backward_it_cannot_run():
+    """When it is built, not at the first backward pass."""
+    adapted(60, False)
+    adapted(64, True)
+    with pytest.raises(ValueError, match="N % 8"):
+        adapted(60, True)
+
+
 def test_a_gradient_of_another_type_is_refused_by_its_name():
     """An fp32 gradient of fp32 outputs of bf16 weights."""
     lin = adapted(64, True)
