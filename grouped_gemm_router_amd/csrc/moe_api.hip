@@ -451,6 +451,8 @@ moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void 
   if (!aligned16(ws)) return MOE_ERR_INVALID;
   // dx is written before dy and x are read for the last time
   if (T > 0 && dx && (dx == dy || dx == x)) return MOE_ERR_INVALID;
+  // u is written before v is read
+  if (T > 0 && dA && u == v) return MOE_ERR_INVALID;
   if (T == 0 && !dA) return MOE_OK;
   const hipStream_t s = as_stream(stream);
   const LoraPlan p = lora_plan(T, N, K, r, n, size_of(dt), true);

@@ -1,6 +1,8 @@
 """CPU checks of the layer's training methods and of the adapters' binding:
 what they pass on and what they refuse, with the library's calls recorded
 instead of made."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -104,3 +106,10 @@ def test_the_binding_names_a_dy_of_another_type(monkeypatch):
     with pytest.raises(TypeError, match="dy"):
         api.moe_lora_linear_backward(z(T, 64), z(T, 16, dtype=torch.bfloat16), A, B, z(2),
                                      z(T, dtype=torch.int32), z(T, 8), z(T, 8))
+
+
+def test_u_over_v_is_refused():
+    """u is written before dB is summed from v."""
+    P, P2, P3, NUL = (C.c_void_p(a) for a in (0x10000, 0x20000, 0x30000, 0))
+    assert api.lib.moe_lora_linear_backward(P, P, P, 0, P, P, api.MOE_BF16, P, P, P3, 16, 64, 64, 8, 2,
+                                            P3, P2, P, P, P, 1 << 40, NUL) == api.MOE_ERR_INVALID
