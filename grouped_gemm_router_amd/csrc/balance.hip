@@ -302,7 +302,10 @@ __global__ __launch_bounds__(kThreadsP) void balance_partial_kernel(
 // ---------------------------------------------------------------------------
 // loss, second launch: workgroup (s, 64 experts) adds its sequence's slots
 // in a fixed order; the last workgroup to finish adds the sequences' losses,
-// again in a fixed order.
+// again in a fixed order.  What a thread adds over its loop is held in 64 bits:
+// a sequence may have a million slots of much the same size, whose roundings in
+// 32 bits all fall on one side (2^24 equal tokens of 2 experts: 2^-14 of a
+// probability).
 // ---------------------------------------------------------------------------
 constexpr int kGroupsF = 16;  // waves per workgroup, each a share of the slots
 
@@ -323,6 +326,7 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
   float p = 0.f;
   int c = 0, n = 0;
   if (lo < hi) {
+    double all = 0.;
     const int k1 = (hi - 1) / C;
     constexpr int U = 4;
     for (int k0 = lo / C + g; k0 <= k1; k0 += U * kGroupsF) {
@@ -338,12 +342,15 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
         cv[u] = in && e < E ? slot_c[at * E + e] : 0;
       }
 #pragma unroll
+      for (int u = 1; u < U; ++u) pv[0] += pv[u];
+      all += (double)pv[0];
+#pragma unroll
       for (int u = 0; u < U; ++u) {
-        p += pv[u];
         c += cv[u];
         n += nv[u];
       }
     }
+    p = (float)all;
   }
   s_p[g][lane] = p;
   s_c[g][lane] = c;
@@ -358,13 +365,12 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
       c += s_c[w][lane];
       n += s_n[w];
     }
-    const float fn = (float)max(n, 1);
-    p = p / fn;
+    const float fn = (float)max(n, 1), mean = p / fn;
     if (e < E) {
       counts[(size_t)s * E + e] = c;
-      probs[(size_t)s * E + e] = p;
+      probs[(size_t)s * E + e] = mean;
     }
-    const float d = wave_sum(e < E ? (float)c / (fn * (float)k) * p : 0.f);
+    const float d = wave_sum(e < E ? (float)c / (fn * (float)k) * mean : 0.f);
     if (lane == 0) {
       // read by the last workgroup, perhaps on another XCD
       __hip_atomic_store(&dots[blockIdx.x], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -379,13 +385,13 @@ __global__ __launch_bounds__(kGroupsF *kWave) void balance_final_kernel(
   }
   __syncthreads();
   if (!s_last) return;
-  float sum = 0.f;
+  double part = 0.;
   int some = 0;
   for (int i = tid; i < (int)gridDim.x; i += kGroupsF * kWave)  // (0 for an empty sequence)
-    sum += __hip_atomic_load(&dots[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    part += (double)__hip_atomic_load(&dots[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   for (int i = tid; i < S; i += kGroupsF * kWave)
     some += __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
-  sum = wave_sum(sum);
+  float sum = wave_sum((float)part);
   for (int o = 32; o > 0; o >>= 1) some += __shfl_xor(some, o, kWave);
   if (lane == 0) {
     s_p[0][g] = sum;

@@ -44,9 +44,10 @@ extern "C" {
  *
  * logits [T][E] fp32 (16-byte aligned), topk_idx [T][k] int32; counts [S][E]
  * int32, probs [S][E] fp32, tokens [S+1] int32 and loss [1] fp32 are
- * written.  Sums in fp32 in a fixed order; counts are exact.  One sequence
- * over the whole batch without a mask gives moe_router_stats' P and loss up
- * to the order of the sums.
+ * written.  Sums in a fixed order, in fp32 or more; what they lose does not
+ * grow with T.  Counts are exact.  One sequence over the whole batch
+ * without a mask gives moe_router_stats' P and loss up to the rounding of the
+ * sums.
  * ws (device, 4-byte aligned) must hold moe_balance_loss_workspace_size(T,
  * E, S) bytes (else MOE_ERR_WORKSPACE); calls that share it must be ordered.
  * Requires 1 <= k <= min(E, MOE_MAX_TOPK), E <= MOE_MAX_EXPERTS,
