@@ -26,7 +26,10 @@ constexpr int kThreadsP = kWavesP * kWave;
 
 // e^x for x <= 0 by the hardware exp2 (within 1 ulp) of the rounded product
 // x log2(e): |x| 2^-24 more, so that the large probabilities, whose x is
-// small, keep all their bits.  -inf gives 0.
+// small, keep all their bits.  -inf gives 0.  (With what the product loses put
+// back, and the normaliser's reciprocal refined, the gradient of 16381 tokens of
+// 256 experts is off by 7.2e-8 of its norm instead of 7.8e-8, and the loss of
+// 32749 tokens takes 23.5 us instead of 21.)
 __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504f);
 }

@@ -583,10 +583,15 @@ __global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
 // at 4 TB/s).
 //
 // rot: workgroups of different columns begin at different K, so that their
-// loads of W do not all hit the same memory channels (W's rows are a power of
-// two apart): 128 rows of 4096 x 14336 36.2 us instead of 38.6.  With more
-// rows the tiles that share x want the same part of it at the same time: 512
-// rows 36.3 us instead of 29.6.
+// loads of W do not all hit the same memory channels.  That is so where W's rows
+// lie a multiple of 4 KB apart, and those rows go this way.  Without / with, us:
+// 128 rows of N 14336, K 4096 39.1 / 36.6, 64 rows 30.2 / 27.7; 64 rows of N
+// 28672, K 4096 57.1 / 45.5, of N and K 8192 46.9 / 41.4, of N 14336, K 6144
+// 46.8 / 40.8.  Other pitches lose by it or gain nothing: the same N and K 8192
+// with 256 bytes behind each row 44.3 / 50.2, N 14336, K 4096 so padded 28.5 /
+// 30.8, dense K 7168 46.1 / 46.3.  With more rows the tiles that share x want the
+// same part of it at the same time: 512 rows of 4096 x 4096 36.3 us instead of
+// 29.6.
 //
 // Pieces past K come from a zero in memory (the last steps only); rows past T
 // and columns past N repeat the last one and are not stored.
@@ -904,7 +909,9 @@ constexpr Shape kShapes[] = {
     {256, 256, 1750, 12000}, {128, 128, 700, 5000}, {64, 128, 480, 4000}, {64, 64, 310, 3000}};
 constexpr int kNumShapes = sizeof(kShapes) / sizeof(kShapes[0]);
 
-// the shape whose rounds over the CUs cost least
+// The shape whose rounds over the CUs cost least.  (Without a W there are no K
+// steps to pay, but the fixed part alone would choose otherwise for one size in
+// 700, so they are counted all the same.)
 int pick_tile(int T, int N, int K, bool with_w, int cus) {
   int best = 1;
   double least = 1e300;
@@ -945,7 +952,7 @@ void launch_bf16(const char *x, const char *W, int ldw, const char *F, const flo
 #undef MOE_ROWS
     return;
   }
-  const int rot = T <= 128;
+  const int rot = T <= 128 && (size_t)ldw * 2 % 4096 == 0;
 #define MOE_TILES(kernel, BM, BNT) \
   launch_tiles(kernel, 256, BM, BNT, x, W, ldw, F, v, adapter, order, T, N, K, r, n, y, s, rot)
   switch (pick_tile(T, N, K, W != nullptr, cus)) {

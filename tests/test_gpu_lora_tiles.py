@@ -1,13 +1,14 @@
 """GPU parity of the adapters' kernels that the size lists of test_gpu_lora.py
 do not choose: fp32 tiles of 64 x 64, which run from as many tiles as the GPU
 has compute units on, and fp32 batches whose rows the forward pass sorts
-(more than 250 MB of factors to read row by row).  References and tolerances
-are those of test_gpu_lora.py."""
+(more than 250 MB of factors to read row by row); and the row pitches of W
+that bf16 tiles treat apart.  References and tolerances are those of
+test_gpu_lora.py."""
 import pytest
 import torch
 
 from gpu_util import DEV
-from test_gpu_lora import F32, Case, check_backward, check_forward, forward
+from test_gpu_lora import BF, F32, Case, check_backward, check_forward, forward
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,14 @@ def test_one_request_never_meets_another_wide(r):
     keep = (c.adapter != 2) & (torch.arange(1300) != 650)
     assert torch.equal(y0.cpu()[keep], y1.cpu()[keep])
     assert torch.equal(v0.cpu()[keep], v1.cpu()[keep])
+
+
+@pytest.mark.parametrize("T,N,K,pad", [
+    # rows of W a multiple of 4 KB apart, where workgroups begin at different K:
+    # dense, and behind 1984 columns of 2048 (and 2040, which end inside a step)
+    (40, 264, 2048, 0), (128, 1000, 4096, 0), (100, 520, 1984, 64), (64, 300, 2040, 8),
+    # other pitches, and rows one too many
+    (40, 264, 2048, 128), (128, 1000, 4096, 128), (129, 264, 2048, 0)])
+def test_forward_bf16_row_pitches(T, N, K, pad):
+    print("lora pitch", T, N, K, pad, flush=True)
+    check_forward(Case(T, N, K, 16, 5, BF, "mixed", T + N).gpu(), BF, ldw_pad=pad)
