@@ -3,9 +3,11 @@
 :class:`AdaptedLinear` keeps the weights where the library's calls take them
 (``include/moe_lora.h``) and allocates the outputs; every step runs in the
 library's HIP kernels on the current stream, with no host synchronisation.
-It serves any shared projection next to the expert layer: attention's, a
-shared expert's, or the router itself (fp32 logits for
-``MOE_ROUTE_FROM_LOGITS``).
+It serves a projection that the caller runs beside the expert layer
+(attention's, say), or a router whose fp32 logits the caller hands to
+``moe_route`` with ``MOE_ROUTE_FROM_LOGITS``.  ``MoELayer`` itself computes its
+own logits and runs its shared experts inside the grouped GEMMs, both without
+adapters.
 """
 from __future__ import annotations
 

@@ -12,7 +12,7 @@
 // stream: it is one burst of loads between its start and its end, so what
 // counts is that every load is issued before anything is looked up, that the
 // code is short, and that the sums over a token's lanes are DPP.  Measured:
-// loss of 32749 tokens of 256 experts (34 MB) 16.0 + 5.2 us, of 256 tokens of
+// loss of 32749 tokens of 256 experts (34 MB) 15.9 + 5.3 us, of 256 tokens of
 // 8 3.7 us; gradient of 16381 tokens of 256 (34 MB) 12.6 us, of 4096 of 8
 // 4.0 us.
 #include "balance_internal.h"

@@ -8,9 +8,11 @@
 // The low-rank part of a 32-row block of one or a few adapters (rows come
 // sorted by adapter) goes through the matrix cores: v is split into bf16
 // terms (two for a bf16 y, three for an fp32 y, so that the product keeps 16
-// or 24 bits of v) and multiplied like 16 more columns of x.  In a block of
-// many adapters every row reads its own adapter's rows of F on the vector
-// ALUs.  An infinity or NaN in one request's adapter stays in that request's
+// or 24 bits of v) and multiplied like 16 more columns of x.  (Three for a bf16
+// y, which rounds to 8 bits: 1331 rows of rank 64 78.3 us instead of 75.4, 777
+// rows of 33 adapters of rank 32 58.6 -> 60.4, 4096 rows of rank 16 141.7 instead
+// of 141.0; the error of y stays.)  In a block of many adapters every row reads
+// its own adapter's rows of F on the vector ALUs, with all of v.  An infinity or NaN in one request's adapter stays in that request's
 // rows, and changes no bit of the others.
 #include "lora_tile.h"
 
@@ -142,9 +144,12 @@ __device__ __forceinline__ void find_kinds(TileKinds &tk, const int *s_ad, int b
 // columns) are staged in LDS as the matrix cores' fragments, up to RC ranks of
 // all the tile's adapters at once.  What counts here is the number of
 // instructions: the code runs once a tile, from beyond the instruction cache,
-// where it arrives at some 50 ns per 64 bytes.  Measured per tile: 16 ranks of
-// one adapter on 256 x 256 6.6 us, with fragments built from single elements
-// 9.2; 32 ranks of 2 to 3 adapters a block on 128 x 128 6.9 us, so built 9.2.
+// where it arrives at some 50 ns per 64 bytes.  By clock stamps inside a tile: 16
+// ranks of one adapter on 256 x 256 6.6 us, with fragments built from single
+// elements 9.2; 32 ranks of 2 to 3 adapters a block on 128 x 128 6.9 us, so built
+// 9.2.  The launch grows by more: 4096 rows, N 4096, rank 16 by 10 us, 1331 rows,
+// N 2048, rank 64 by 7, 777 rows of 33 adapters, N 7168, rank 32 by 13.5 (two
+// rounds of tiles).
 //
 // v_of(row): 256 bytes for a row of the tile; slab_of(i), i < NSLAB: SLAB
 // bytes each.  s_row, s_ad: the tile's rows and adapters (-1 for none).
@@ -577,10 +582,13 @@ __global__ __launch_bounds__(kF32Waves *kWave) void expand_f32_small_kernel(
 // through a ring of four slots of one 64-deep K step each, one barrier a step.
 // The ring's slots are separate LDS arrays, so that the compiler does not wait
 // for a load into one slot before it reads another.  What bounds it is the
-// rate at which a CU takes in operands: 50 to 60 bytes a ns whatever the shape
-// (1331 rows, N 2048, K 7168 on 128 x 128: 50 us for 112 steps of 32 KB on 176
-// CUs, the matrix cores busy 46 % of it; 128 rows, N 14336, K 4096: W streams
-// at 4 TB/s).
+// rate at which a CU takes in operands: about 80 bytes a ns where they come from
+// L2 and the memory-side cache, whatever the shape, 50 to 65 with all CUs on
+// 128 x 128 and a long K.  1331 rows, N 2048, K 7168 on 128 x 128 without
+// adapters: 51 us, 42 of them for 112 steps of 32 KB on 176 CUs (with rank 64
+// 62 us, the matrix cores busy 27 % of the chip's cycles, 39 % of those of the
+// CUs that have a tile).  128 rows, N 14336, K 4096 without adapters: 36 us, W
+// from HBM at 3.3 TB/s.
 //
 // rot: workgroups of different columns begin at different K, so that their
 // loads of W do not all hit the same memory channels.  That is so where W's rows
@@ -740,9 +748,10 @@ __global__ __launch_bounds__(256) void expand_ring_kernel(
 // ---------------------------------------------------------------------------
 // bf16, large batches: 256 x 256 tiles (four waves of 128 x 128, which read
 // half as many operand bytes from LDS per multiply as 64 x 64).  K % 128 == 0.
-// 4096 rows, N and K 4096, one tile a CU: 97 us of K loop (the matrix cores
-// busy 63 % of it at the clock that this load leaves), 7 of low-rank part, 10
-// of y, at the rate of HBM.
+// 4096 rows, N and K 4096, one tile a CU, rank 16: 124 to 131 us, the matrix
+// cores busy 53 % of it at the 1.9 GHz that this load leaves.  Without adapters
+// 115: 17 before and behind the K loop (start, rows, y), 98 in it (23 per 1024 of
+// K up to 2048, 26 from there on).
 // ---------------------------------------------------------------------------
 template <int OS>
 __global__ __launch_bounds__(256, 1) void expand_big_kernel(
@@ -899,9 +908,11 @@ __global__ __launch_bounds__(kRowWaves *kWave) void expand_rows_kernel(
 // 27.7 us here, 80 rows 23.4 us in tiles; 32 rows 18.9 us here).
 constexpr int kExpandRowsMax = 32;
 
-// Tile shapes of the bf16 kernels, and what a 64-deep K step and the rest of a
-// tile take on a CU, in ns: measured with one tile per CU on 96 to 4096 rows,
-// K from 2048 to 7168.
+// Tile shapes of the bf16 kernels, and what pick_tile counts for a 64-deep K
+// step and for the rest of a tile on a CU, in ns: measured with one tile per CU
+// on 96 to 4096 rows, K from 2048 to 7168.  256 tiles whose operands stay in the
+// memory-side cache take 1650, 490 to 640, 300 and 195 ns a step and 16, 7.6, 6.1
+// and 5 us for the rest, so the smaller shapes are counted rather dear.
 struct Shape {
   int BM, BN, step, fixed;
 };

@@ -64,8 +64,8 @@ struct LoraPlan {
   int TS, max_units, max_tiles;
 };
 
-// rows per unit: at most 64 slices to add; batches of up to 1024 rows are
-// never sliced and need no launch that adds slices
+// rows per unit: at most 32 slices of an adapter to add; batches of up to 1024
+// rows are never sliced and need no launch that adds slices
 inline LoraPlan lora_plan(int T, int N, int K, int r, int n, int es, bool backward) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   LoraPlan p;

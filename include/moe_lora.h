@@ -18,7 +18,9 @@
  * the column j of the usual [N][r] matrix): the forward and the backward pass
  * then read each of them along rows only.  An adapter of a lower rank than r
  * has zero rows behind it.  x, W, A and B are of one type dt, MOE_BF16 or
- * MOE_F32; products accumulate in fp32, and v and u are fp32.
+ * MOE_F32; products accumulate in fp32, and v and u are fp32.  Where a bf16 y
+ * or dx is computed, v (u) may enter the product with its upper 16 bits only,
+ * 2^-16 of each term; everywhere else with all 24.
  * An infinity or NaN in a row of x or in an adapter stays in the rows that
  * use it and changes no bit of the others; in those rows it gives an infinity
  * or a NaN, which of them is not specified.  Outputs must not overlap inputs.
@@ -66,7 +68,8 @@ size_t moe_lora_linear_workspace_size(int T, int N, int K, int r, int n, moe_dty
  *   dA[a][j] = sum over the rows t of a of u[t][j] x[t]    [K]
  *   dB[a][j] = sum over the rows t of a of v[t][j] dy[t]   [N]
  * dy [T][N], x [T][K] and v [T][r] as in the forward pass; W_t [K][N] is W
- * transposed (row pitch ldw, 0 meaning N), all of type dt.  dx [T][K] of type
+ * transposed (row pitch ldw, 0 meaning N), all but v of type dt (so dy is too
+ * where y was fp32 beside bf16 factors: the caller rounds it).  dx [T][K] of type
  * dt or NULL; W_t == NULL adds the adapters' part to dx in place.  dA [n][r][K]
  * and dB [n][r][N], both fp32, are both written or both NULL; an adapter
  * without rows gets zeros (all of them for T == 0).  u [T][r] fp32 is written.  Requires N % 8 == 0
