@@ -87,14 +87,23 @@ inline LoraPlan lora_plan(int T, int N, int K, int r, int n, int es, bool backwa
   return p;
 }
 
-// Whether the forward pass reads its rows through a plan: not where reading
-// every row's factors, the most that rows in any order can cost, takes less
-// than the plan's launch and the longer way through it.  Measured in order /
-// through a plan, us: 128 rows of N 14336, K 4096 (75e6 bytes) 48 / 55; N and
-// K 4096: 512 rows of rank 16 (134e6) 39 / 44 on 64 adapters, 37 / 40 on 8;
-// 1024 rows (268e6) 65 / 62 on 100 adapters, 66 / 67 on 160.
+// Whether the forward pass reads its rows through a plan: not where a wave per
+// row and rank takes less than the plan's launch and the longer way through it.
+// That is so up to a number of waves, whatever N and K are (they cost their
+// launch even where a row is short), and up to the bytes that rows in any order
+// can cost.  Measured in order / through a plan, us, rows in any order:
+//   bf16, T r = 8192, 16384, 32768, 131072: K and N 64, r 8 13.8 / 17.4, 18.6 /
+//   18.5, 28.3 / 21.0, 84 / 40; K 512, N 512, r 64 21.3 / 20.5, 26.1 / 20.3, 35.2 /
+//   21.5, 88 / 23; K and N 2048, r 16 19.6 / 24.4, 31.1 / 30.2, 52.5 / 38.8, 174 / 94;
+//   fp32, T r = 16384, 32768, 131072: K 256, N 64, r 8 15.9 / 16.3, 23.8 / 19.0,
+//   83 / 47; K 512, N 512, r 64 20.0 / 26.5, 26.5 / 27.9, 91 / 45; K 2048, N 512,
+//   r 16 52.5 / 48.8, 89 / 81, 331 / 295;
+//   bytes, bf16: 128 rows of N 14336, K 4096 (75e6) 48 / 55; N and K 4096: 512 rows
+//   of rank 16 (134e6) 39 / 44 on 64 adapters, 37 / 40 on 8; 1024 rows (268e6) 65 /
+//   62 on 100 adapters, 66 / 67 on 160.
 inline bool lora_sorts(int T, int N, int K, int r, int es) {
-  return (double)T * r * ((double)N + K) * es > 250e6;
+  return (long long)T * r >= (es == 2 ? 16384 : 32768) ||
+         (double)T * r * ((double)N + K) * es > 250e6;
 }
 
 hipError_t launch_lora_plan(const int32_t *adapter, int T, int n, const LoraPlan &p, bool units,

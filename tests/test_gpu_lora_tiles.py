@@ -80,3 +80,15 @@ def test_one_request_never_meets_another_wide(r):
 def test_forward_bf16_row_pitches(T, N, K, pad):
     print("lora pitch", T, N, K, pad, flush=True)
     check_forward(Case(T, N, K, 16, 5, BF, "mixed", T + N).gpu(), BF, ldw_pad=pad)
+
+
+@pytest.mark.parametrize("kind", ["requests", "mixed"])
+@pytest.mark.parametrize("dt,T,N,K,r,n", [
+    (BF, 2049, 40, 64, 128, 8), (BF, 8200, 8, 8, 8, 3), (BF, 300, 65, 72, 56, 700),
+    (BF, 128, 33, 16, 128, 2), (F32, 2049, 40, 64, 128, 8), (F32, 4100, 17, 8, 8, 90)])
+def test_many_rows_of_short_factors(dt, T, N, K, r, n, kind):
+    """Batches that are sorted for their number of rows and ranks alone."""
+    print("lora short", dt, T, N, K, r, n, kind, flush=True)
+    c = Case(T, N, K, r, n, dt, kind, T).gpu()
+    check_forward(c, dt)
+    check_forward(c, F32, with_w=False)

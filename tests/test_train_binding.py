@@ -113,3 +113,13 @@ def test_u_over_v_is_refused():
     P, P2, P3, NUL = (C.c_void_p(a) for a in (0x10000, 0x20000, 0x30000, 0))
     assert api.lib.moe_lora_linear_backward(P, P, P, 0, P, P, api.MOE_BF16, P, P, P3, 16, 64, 64, 8, 2,
                                             P3, P2, P, P, P, 1 << 40, NUL) == api.MOE_ERR_INVALID
+
+
+def test_many_rows_of_short_factors_are_sorted():
+    """Rows that are sorted have a plan, in the workspace: large batches
+    whatever N and K are, not small ones."""
+    size = api.moe_lora_linear_workspace_size
+    bf, f32 = torch.bfloat16, torch.float32
+    assert size(8192, 40, 64, 128, 8, bf) > 0 and size(8192, 8, 8, 8, 8, bf) > 0
+    assert size(4096, 40, 64, 128, 8, f32) > 0
+    assert size(256, 256, 128, 8, 4, f32) == 0 and size(128, 512, 512, 16, 64, bf) == 0
