@@ -32,7 +32,13 @@ EXPORTS = ["moe_status_string", "moe_abi_version", "moe_route_workspace_size", "
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
            # include/moe_lora.h
            "moe_lora_linear_workspace_size", "moe_lora_linear",
-           "moe_lora_backward_workspace_size", "moe_lora_linear_backward"]
+           "moe_lora_backward_workspace_size", "moe_lora_linear_backward",
+           # include/moe_backward.h
+           "moe_combine_backward", "moe_permute_backward",
+           "moe_grouped_gemm_dgrad_workspace_size", "moe_grouped_gemm_dgrad",
+           "moe_grouped_gemm_dgrad_swiglu",
+           "moe_grouped_gemm_wgrad_workspace_size", "moe_grouped_gemm_wgrad",
+           "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_grad_clip"]
 
 
 class MoEError(RuntimeError):
@@ -100,6 +106,29 @@ def _load():
     lib.moe_lora_linear_backward.restype = i32
     lib.moe_lora_linear_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, i32, i32,
                                              i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_combine_backward.restype = i32
+    lib.moe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+    lib.moe_permute_backward.restype = i32
+    lib.moe_permute_backward.argtypes = [vp, i32, vp, i32, i32, i32, i32, vp, vp, i32, vp]
+    lib.moe_grouped_gemm_dgrad_workspace_size.restype = sz
+    lib.moe_grouped_gemm_dgrad_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.moe_grouped_gemm_dgrad.restype = i32
+    lib.moe_grouped_gemm_dgrad.argtypes = [vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32,
+                                           i32, vp, sz, vp]
+    lib.moe_grouped_gemm_dgrad_swiglu.restype = i32
+    lib.moe_grouped_gemm_dgrad_swiglu.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i32,
+                                                  i32, i32, i32, vp, sz, vp]
+    lib.moe_grouped_gemm_wgrad_workspace_size.restype = sz
+    lib.moe_grouped_gemm_wgrad_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.moe_grouped_gemm_wgrad.restype = i32
+    lib.moe_grouped_gemm_wgrad.argtypes = [vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, vp,
+                                           sz, vp]
+    lib.moe_grad_norm_workspace_size.restype = sz
+    lib.moe_grad_norm_workspace_size.argtypes = [i32]
+    lib.moe_grad_norm.restype = i32
+    lib.moe_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.moe_grad_clip.restype = i32
+    lib.moe_grad_clip.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp]
     if lib.moe_abi_version() != ABI_VERSION:
         raise ImportError("libmoe.so ABI version %d, binding expects %d"
                           % (lib.moe_abi_version(), ABI_VERSION))
@@ -366,8 +395,9 @@ def moe_quantize_fp8(src, q, scale, *, block_rows=128, block_cols=128, stream=No
 
 
 # ----------------------------------------------------------------------------
-# include/moe_balance.h and include/moe_lora.h.  Every tensor is checked for
-# its type, shape, contiguity and device before the library is called.
+# include/moe_balance.h, include/moe_lora.h and include/moe_backward.h.  Every
+# tensor is checked for its type, shape, contiguity and device before the
+# library is called.
 # ----------------------------------------------------------------------------
 
 def _arg(t, name, dtype, shape, device):
@@ -579,4 +609,191 @@ def moe_lora_linear_backward(dy, x, A, B, scale, adapter, v, u, *, W_t=None, dx=
                    _arg(u, "u", f32, (T, r), dev), _arg(dx, "dx", dt, (T, K), dev),
                    _arg(dA, "dA", f32, (n, r, K), dev),
                    _arg(dB, "dB", f32, (n, r, N), dev), ws.data_ptr(), ws_bytes,
+                   _raw_stream(stream, dev))
+
+
+def moe_combine_backward(d_out, Y, flat_to_row, topk_w, dY, d_topk_w, *, n_shared=0, stream=None):
+    """Gradient of moe_combine from d_out [T][d] (bf16 or fp32): dY [T k +
+    n_shared T][d] of d_out's type and d_topk_w [T][k] fp32 are written.  Y and
+    flat_to_row as moe_combine read them.  dY None (only the gate weights'
+    gradient), or d_topk_w None with Y None (only the rows')."""
+    T, d = d_out.shape
+    k = topk_w.shape[1]
+    rows = T * (k + n_shared)
+    dev = _gpu(d_out, "d_out")
+    if (Y is None) != (d_topk_w is None):
+        raise ValueError("Y and d_topk_w are given together")
+    dt, y_dt = _act(d_out, "d_out"), MOE_F32 if Y is None else _act(Y, "Y")
+    return _invoke("moe_combine_backward", lib.moe_combine_backward,
+                   _arg(d_out, "d_out", d_out.dtype, (T, d), dev), dt,
+                   _arg(Y, "Y", None if Y is None else Y.dtype, (rows, d), dev), y_dt,
+                   _arg(flat_to_row, "flat_to_row", torch.int32, (rows,), dev),
+                   _arg(topk_w, "topk_w", torch.float32, (T, k), dev), T, k, d, n_shared,
+                   _arg(dY, "dY", d_out.dtype, (rows, d), dev),
+                   _arg(d_topk_w, "d_topk_w", torch.float32, (T, k), dev), _raw_stream(stream, dev))
+
+
+def moe_permute_backward(dx_perm, flat_to_row, dx, k, *, n_shared=0, addend=None, stream=None):
+    """Gradient of moe_permute's row copies: dx [T][d] = the sum of each
+    token's rows of dx_perm [T k + n_shared T][d] (bf16 or fp32 each), plus
+    addend [T][d] of dx's type if given (it may be dx)."""
+    T, d = dx.shape
+    rows = T * (k + n_shared)
+    dev = _gpu(dx, "dx")
+    return _invoke("moe_permute_backward", lib.moe_permute_backward,
+                   _arg(dx_perm, "dx_perm", dx_perm.dtype, (rows, d), dev),
+                   _act(dx_perm, "dx_perm"),
+                   _arg(flat_to_row, "flat_to_row", torch.int32, (rows,), dev), T, k, d, n_shared,
+                   _arg(addend, "addend", dx.dtype, (T, d), dev),
+                   _arg(dx, "dx", dx.dtype, (T, d), dev), _act(dx, "dx"), _raw_stream(stream, dev))
+
+
+def _act(t, name) -> int:
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+
+
+def _experts(B, name, dtype, N, device):
+    """(pointer, G, K, row pitch) of [G][N][K] weights whose rows may be padded."""
+    if not isinstance(B, torch.Tensor) or B.dim() != 3 or B.dtype != dtype:
+        raise TypeError("%s must be a [G][N][K] %s tensor" % (name, dtype))
+    if B.shape[1] != N:
+        raise ValueError("%s must have %d rows an expert, got %s" % (name, N, list(B.shape)))
+    if B.get_device() != device:
+        raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
+    p, _, ldb = _weights(B)
+    return p, B.shape[0], B.shape[2], ldb
+
+
+def _own_workspace(ws, size, device, stream):
+    """(pointer, bytes) of a workspace that may be of size 0."""
+    if size == 0 and ws is None:
+        return None, 0, None
+    ws, ws_bytes = _workspace(ws, size, device, stream)
+    return ws.data_ptr(), ws_bytes, ws
+
+
+def moe_grouped_gemm_dgrad_workspace_size(G: int, rows: int, N: int, K: int, dtype) -> int:
+    return int(lib.moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, _lora_dt(dtype)))
+
+
+def moe_grouped_gemm_dgrad(dC, B, dA, offsets, *, dC2=None, B2=None, ws=None, stream=None):
+    """Gradient of moe_grouped_gemm's input: dA[r] = dC[r] B[g] (+ dC2[r]
+    B2[g]) for the rows r of group g.  dC, dC2 [rows][N], B, B2 [G][N][K] (rows
+    may be padded) of one type, dA [rows][K] of that type or fp32.  ws:
+    moe_grouped_gemm_dgrad_workspace_size bytes; when None, one is allocated
+    here for this call."""
+    rows, N = dC.shape
+    dt = dC.dtype
+    dev = _gpu(dC, "dC")
+    p, G, K, ldb = _experts(B, "B", dt, N, dev)
+    p2 = None
+    if B2 is not None:
+        p2, *rest = _experts(B2, "B2", dt, N, dev)
+        if rest != [G, K, ldb]:
+            raise ValueError("B2 must have B's shape and strides")
+    if dA.dtype not in (dt, torch.float32):
+        raise TypeError("dA must be %s or %s, got %s" % (dt, torch.float32, dA.dtype))
+    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt), dev,
+                                stream)
+    return _invoke("moe_grouped_gemm_dgrad", lib.moe_grouped_gemm_dgrad,
+                   _arg(dC, "dC", dt, (rows, N), dev), p,
+                   _arg(dC2, "dC2", dt, (rows, N), dev), p2, _act(dC, "dC"),
+                   _arg(dA, "dA", dA.dtype, (rows, K), dev), _act(dA, "dA"),
+                   _arg(offsets, "offsets", torch.int32, (G + 1,), dev), G, rows, N, K, ldb, pw, wb,
+                   _raw_stream(stream, dev))
+
+
+def moe_grouped_gemm_dgrad_swiglu(dC, B, gate, up, d_gate, d_up, offsets, *, h=None, ws=None,
+                                  stream=None):
+    """moe_grouped_gemm_dgrad for an input that was silu(gate) * up: writes
+    d_gate and d_up, and h = silu(gate) * up if given.  gate, up, d_gate, d_up,
+    h [rows][K] of dC's type; d_gate may be gate, and d_up may be up."""
+    rows, N = dC.shape
+    dt = dC.dtype
+    dev = _gpu(dC, "dC")
+    p, G, K, ldb = _experts(B, "B", dt, N, dev)
+    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt), dev,
+                                stream)
+    of = (rows, K)
+    return _invoke("moe_grouped_gemm_dgrad_swiglu", lib.moe_grouped_gemm_dgrad_swiglu,
+                   _arg(dC, "dC", dt, (rows, N), dev), p, _act(dC, "dC"),
+                   _arg(gate, "gate", dt, of, dev), _arg(up, "up", dt, of, dev),
+                   _arg(d_gate, "d_gate", dt, of, dev), _arg(d_up, "d_up", dt, of, dev),
+                   _arg(h, "h", dt, of, dev),
+                   _arg(offsets, "offsets", torch.int32, (G + 1,), dev), G, rows, N, K, ldb, pw, wb,
+                   _raw_stream(stream, dev))
+
+
+def moe_grouped_gemm_wgrad_workspace_size(G: int, rows: int, N: int, K: int, dtype) -> int:
+    return int(lib.moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, _lora_dt(dtype)))
+
+
+def moe_grouped_gemm_wgrad(dC, A, dB, offsets, *, accumulate=False, ws=None, stream=None):
+    """Gradient of moe_grouped_gemm's weights: dB[g] = sum of dC[r]^T A[r] over
+    the rows r of group g (accumulate: added to dB).  dC [rows][N], A [rows][K]
+    of one type, dB [G][N][K] of that type or fp32.  ws:
+    moe_grouped_gemm_wgrad_workspace_size bytes; when None, one is allocated
+    here for this call."""
+    rows, N = dC.shape
+    K = A.shape[1]
+    G = dB.shape[0]
+    dt = dC.dtype
+    dev = _gpu(dB, "dB")
+    if dB.dtype not in (dt, torch.float32):
+        raise TypeError("dB must be %s or %s, got %s" % (dt, torch.float32, dB.dtype))
+    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, dt), dev,
+                                stream)
+    return _invoke("moe_grouped_gemm_wgrad", lib.moe_grouped_gemm_wgrad,
+                   _arg(dC, "dC", dt, (rows, N), dev), _arg(A, "A", dt, (rows, K), dev),
+                   _act(dC, "dC"), _arg(dB, "dB", dB.dtype, (G, N, K), dev), _act(dB, "dB"),
+                   _arg(offsets, "offsets", torch.int32, (G + 1,), dev), G, rows, N, K,
+                   1 if accumulate else 0, pw, wb, _raw_stream(stream, dev))
+
+
+def _grads(grads, name, device):
+    """Host arrays (pointers, sizes, types) of a list of gradients."""
+    n = len(grads)
+    ptrs, sizes, dts = (C.c_void_p * n)(), (C.c_int64 * n)(), (C.c_int * n)()
+    for i, t in enumerate(grads):
+        if t.get_device() != device:
+            raise ValueError("%s[%d] must be on GPU %d, like norm" % (name, i, device))
+        if not t.is_contiguous():
+            raise ValueError("%s[%d] must be contiguous" % (name, i))
+        ptrs[i], sizes[i], dts[i] = t.data_ptr(), t.numel(), _act(t, name)
+    return ptrs, sizes, dts
+
+
+def moe_grad_norm_workspace_size(n: int) -> int:
+    return int(lib.moe_grad_norm_workspace_size(n))
+
+
+def moe_grad_norm(grads, norm, *, ws=None, stream=None):
+    """norm [1] fp32 = the 2-norm over all elements of a list of gradients
+    (bf16 or fp32, of any shapes, contiguous).  ws:
+    moe_grad_norm_workspace_size(len(grads)) bytes; when None, one is allocated
+    here for this call."""
+    dev = _gpu(norm, "norm")
+    ptrs, sizes, dts = _grads(grads, "grads", dev)
+    pw, wb, ws = _own_workspace(ws, moe_grad_norm_workspace_size(len(grads)), dev, stream)
+    return _invoke("moe_grad_norm", lib.moe_grad_norm, ptrs, sizes, dts, len(grads),
+                   _arg(norm, "norm", torch.float32, (1,), dev), pw, wb, _raw_stream(stream, dev))
+
+
+def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
+    """Scale every gradient by min(1, max_norm / (norm + 1e-6)), norm [1] fp32
+    on the device: in place, or into the tensors of out (of the gradients'
+    sizes and types; one may be its gradient)."""
+    dev = _gpu(norm, "norm")
+    ptrs, sizes, dts = _grads(grads, "grads", dev)
+    outs = None
+    if out is not None:
+        outs, osizes, odts = _grads(out, "out", dev)
+        if osizes[:] != sizes[:] or odts[:] != dts[:]:
+            raise ValueError("out must have the gradients' sizes and types")
+    return _invoke("moe_grad_clip", lib.moe_grad_clip, ptrs, sizes, dts, len(grads),
+                   _arg(norm, "norm", torch.float32, (1,), dev), float(max_norm), outs,
                    _raw_stream(stream, dev))

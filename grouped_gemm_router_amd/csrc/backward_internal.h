@@ -1,0 +1,70 @@
+// backward_internal.h -- host launchers of the backward pass, the global norm
+// and the clipping (include/moe_backward.h).  Arguments are validated by the
+// C-ABI layer before these are called.
+#pragma once
+
+#include "../../include/moe_backward.h"
+#include "moe_internal.h"
+
+hipError_t launch_combine_backward(const void *d_out, int dt, const void *Y, int y_dt,
+                                   const int32_t *flat_to_row, const float *topk_w, int T, int k,
+                                   int d, int n_shared, void *dY, float *d_topk_w, hipStream_t s);
+hipError_t launch_permute_backward(const void *dx_perm, int p_dt, const int32_t *flat_to_row, int T,
+                                   int k, int d, int n_shared, const void *addend, void *dx, int dt,
+                                   hipStream_t s);
+
+// What the products' gradients work on.  dgrad: out [rows][K] = dC B (+ dC2
+// B2); with gate: SwiGLU's gradient, out = d_gate, out2 = d_up, h or null.
+// wgrad: out [G][N][K] (+)= dC^T A per group.
+struct GradArgs {
+  const void *dC = nullptr, *dC2 = nullptr, *B = nullptr, *B2 = nullptr, *A = nullptr;
+  const void *gate = nullptr, *up = nullptr;
+  void *out = nullptr, *out2 = nullptr, *h = nullptr;
+  const int32_t *offsets = nullptr;
+  int G = 0, rows = 0, N = 0, K = 0, ldb = 0;
+  int dt = 0, out_dt = 0;
+  int accumulate = 0;
+  float *part = nullptr;  // wgrad: partial sums [slice][G][N][K], or null
+  int slices = 1;
+};
+
+namespace moe {
+
+// Rows [s[0], s[1]) of group g: group g begins at the largest of
+// clamp(offsets[h], 0, rows) over h <= g, as in the tile scheduler.  The first
+// wave looks at the offsets; s is in LDS.  Must be called by all threads.
+__device__ __forceinline__ void group_rows(const int32_t *__restrict__ offsets, int rows, int g,
+                                           int *s) {
+  if (threadIdx.x < kWave) {
+    int first = 0;
+    for (int h = threadIdx.x; h <= g; h += kWave) first = max(first, min(offsets[h], rows));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) first = max(first, __shfl_xor(first, o, kWave));
+    if (threadIdx.x == 0) {
+      s[0] = first;
+      s[1] = max(first, min(offsets[g + 1], rows));
+    }
+  }
+  __syncthreads();
+}
+
+// The rows of slice i of n: runs of a multiple of 32 rows.
+__device__ __forceinline__ void slice_rows(int *r0, int *r1, int i, int n) {
+  const int per = ((*r1 - *r0 + n - 1) / n + 31) / 32 * 32;
+  const int first = min(*r1, *r0 + i * per);
+  *r1 = min(*r1, first + per);
+  *r0 = first;
+}
+
+}  // namespace moe
+
+hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s);
+hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s);
+// out (+)= the slices' partial sums, in slice order
+hipError_t launch_wgrad_reduce(const GradArgs &a, hipStream_t s);
+
+size_t grad_norm_ws_bytes(int n);
+hipError_t launch_grad_norm(const void *const *grads, const int64_t *sizes, const int *dts, int n,
+                            float *norm, void *ws, hipStream_t s);
+hipError_t launch_grad_clip(const void *const *grads, const int64_t *sizes, const int *dts, int n,
+                            const float *norm, float max_norm, void *const *out, hipStream_t s);

@@ -1,6 +1,6 @@
 // moe_api.hip -- the extern "C" entry points of libmoe.so (declared and
-// documented in include/moe.h, moe_balance.h and moe_lora.h).  Each entry
-// point checks its arguments on the host, returns a status without launching
+// documented in include/moe.h, moe_balance.h, moe_lora.h and
+// moe_backward.h).  Each entry point checks its arguments on the host, returns a status without launching
 // anything if they are bad, and otherwise enqueues the kernels on the
 // caller's stream.  Nothing here allocates, frees, synchronises or reads
 // device memory.
@@ -8,6 +8,7 @@
 
 #include <atomic>
 
+#include "backward_internal.h"
 #include "balance_internal.h"
 #include "lora_internal.h"
 #include "moe_internal.h"
@@ -467,6 +468,200 @@ moe_status_t moe_lora_linear_backward(const void *dy, const void *x, const void 
   if (e == hipSuccess && dA)  // (T == 0: no row of any adapter, zeros)
     e = launch_lora_wgrad(dy, x, dt, u, v, T, N, K, r, n, dA, dB, ws, s);
   return launched(e);
+}
+
+// ---------------------------------------------------------------------------
+// moe_backward.h
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool opt_aligned16(const void *p) { return !p || aligned16(p); }
+
+// sizes of the gradients of moe_combine and moe_permute
+moe_status_t sort_sizes(int T, int k, int d, int n_shared) {
+  if (T < 0 || k < 1 || d < 8 || n_shared < 0) return MOE_ERR_INVALID;
+  if (k > MOE_MAX_TOPK || n_shared > 8 || d % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  // (rows are 32-bit, and a launch has fewer than 2^32 threads)
+  if ((long long)T * (k + n_shared) > INT32_MAX || T >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// sizes of the products' gradients; *ldb becomes the row pitch
+moe_status_t grad_sizes(int G, int rows, int N, int K, int *ldb, moe_dtype_t dt) {
+  if (G < 1 || rows < 0 || N < 1 || K < 1) return MOE_ERR_INVALID;
+  if (!is_act(dt) || G > MOE_MAX_GROUPS || N % 8 != 0 || K % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (*ldb == 0) *ldb = K;
+  if (*ldb < K || (long long)*ldb * size_of(dt) % 16 != 0) return MOE_ERR_INVALID;
+  if ((long long)G * N * *ldb >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+  // (a launch has fewer than 2^32 threads, 256 for each 64 x 64 outputs)
+  const long long tn = (N + 63) / 64, tk = (K + 63) / 64;
+  if ((rows / 64 + (long long)G) * tk >= (1 << 24) || G * tn * tk >= (1 << 24))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t grad_workspace(const void *ws, size_t ws_bytes, size_t need) {
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (ws == nullptr ? ws_bytes != 0 : !aligned16(ws)) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+
+// the host arrays of a list of gradients
+moe_status_t grad_list(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
+                       int n) {
+  if (n < 0) return MOE_ERR_INVALID;
+  if (n > MOE_MAX_GRADS) return MOE_ERR_UNSUPPORTED;
+  if (n > 0 && (!grads || !sizes || !dts)) return MOE_ERR_INVALID;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] < 0) return MOE_ERR_INVALID;
+    if (!is_act(dts[i]) || sizes[i] >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+    if (sizes[i] > 0 &&
+        (!grads[i] || reinterpret_cast<uintptr_t>(grads[i]) % size_of(dts[i]) != 0))
+      return MOE_ERR_INVALID;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void *Y,
+                                  moe_dtype_t y_dt, const int32_t *flat_to_row,
+                                  const float *topk_w, int T, int k, int d, int n_shared, void *dY,
+                                  float *d_topk_w, moe_stream_t stream) {
+  const moe_status_t sizes = sort_sizes(T, k, d, n_shared);
+  if (sizes != MOE_OK) return sizes;
+  if (!is_act(dt) || !is_act(y_dt)) return MOE_ERR_UNSUPPORTED;
+  if (!dY && !d_topk_w) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  if (!aligned16(d_out) || !aligned4(flat_to_row) || !aligned4(topk_w) || !opt_aligned16(dY) ||
+      !opt_aligned4(d_topk_w) || (d_topk_w ? !aligned16(Y) : Y != nullptr))
+    return MOE_ERR_INVALID;
+  if (dY && (dY == d_out || dY == Y)) return MOE_ERR_INVALID;
+  return launched(launch_combine_backward(d_out, dt, Y, y_dt, flat_to_row, topk_w, T, k, d,
+                                          n_shared, dY, d_topk_w, as_stream(stream)));
+}
+
+moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
+                                  const int32_t *flat_to_row, int T, int k, int d, int n_shared,
+                                  const void *addend, void *dx, moe_dtype_t dt,
+                                  moe_stream_t stream) {
+  const moe_status_t sizes = sort_sizes(T, k, d, n_shared);
+  if (sizes != MOE_OK) return sizes;
+  if (!is_act(dt) || !is_act(p_dt)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!aligned16(dx_perm) || !aligned4(flat_to_row) || !opt_aligned16(addend) || !aligned16(dx))
+    return MOE_ERR_INVALID;
+  if (dx == dx_perm) return MOE_ERR_INVALID;
+  return launched(launch_permute_backward(dx_perm, p_dt, flat_to_row, T, k, d, n_shared, addend, dx,
+                                          dt, as_stream(stream)));
+}
+
+size_t moe_grouped_gemm_dgrad_workspace_size(int G, int rows, int N, int K, moe_dtype_t dt) {
+  (void)G, (void)rows, (void)N, (void)K, (void)dt;
+  return 0;
+}
+
+moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *dC2,
+                                    const void *B2, moe_dtype_t dt, void *dA, moe_dtype_t a_dt,
+                                    const int32_t *offsets, int G, int rows, int N, int K, int ldb,
+                                    void *ws, size_t ws_bytes, moe_stream_t stream) {
+  const moe_status_t sizes = grad_sizes(G, rows, N, K, &ldb, dt);
+  if (sizes != MOE_OK) return sizes;
+  if (a_dt != dt && a_dt != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if ((dC2 == nullptr) != (B2 == nullptr)) return MOE_ERR_INVALID;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(dC) || !aligned16(B) || !opt_aligned16(dC2) || !opt_aligned16(B2) ||
+      !aligned16(dA) || !aligned4(offsets))
+    return MOE_ERR_INVALID;
+  if (dA == dC || dA == dC2) return MOE_ERR_INVALID;
+  const moe_status_t space = grad_workspace(
+      ws, ws_bytes, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt));
+  if (space != MOE_OK) return space;
+  GradArgs a;
+  a.dC = dC, a.dC2 = dC2, a.B = B, a.B2 = B2, a.out = dA, a.offsets = offsets;
+  a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb, a.dt = dt, a.out_dt = a_dt;
+  return launched(launch_dgrad_simple(a, as_stream(stream)));
+}
+
+moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dtype_t dt,
+                                           const void *gate, const void *up, void *d_gate,
+                                           void *d_up, void *h, const int32_t *offsets, int G,
+                                           int rows, int N, int K, int ldb, void *ws,
+                                           size_t ws_bytes, moe_stream_t stream) {
+  const moe_status_t sizes = grad_sizes(G, rows, N, K, &ldb, dt);
+  if (sizes != MOE_OK) return sizes;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(dC) || !aligned16(B) || !aligned16(gate) || !aligned16(up) || !aligned16(d_gate) ||
+      !aligned16(d_up) || !opt_aligned16(h) || !aligned4(offsets))
+    return MOE_ERR_INVALID;
+  if (d_gate == dC || d_up == dC || d_gate == d_up || d_gate == up || d_up == gate)
+    return MOE_ERR_INVALID;
+  if (h && (h == dC || h == gate || h == up || h == d_gate || h == d_up)) return MOE_ERR_INVALID;
+  const moe_status_t space = grad_workspace(
+      ws, ws_bytes, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt));
+  if (space != MOE_OK) return space;
+  GradArgs a;
+  a.dC = dC, a.B = B, a.gate = gate, a.up = up, a.out = d_gate, a.out2 = d_up, a.h = h;
+  a.offsets = offsets, a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb;
+  a.dt = dt, a.out_dt = dt;
+  return launched(launch_dgrad_simple(a, as_stream(stream)));
+}
+
+size_t moe_grouped_gemm_wgrad_workspace_size(int G, int rows, int N, int K, moe_dtype_t dt) {
+  (void)G, (void)rows, (void)N, (void)K, (void)dt;
+  return 0;
+}
+
+moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t dt, void *dB,
+                                    moe_dtype_t b_dt, const int32_t *offsets, int G, int rows,
+                                    int N, int K, int accumulate, void *ws, size_t ws_bytes,
+                                    moe_stream_t stream) {
+  int ldb = 0;
+  const moe_status_t sizes = grad_sizes(G, rows, N, K, &ldb, dt);
+  if (sizes != MOE_OK) return sizes;
+  if (b_dt != dt && b_dt != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!aligned16(dC) || !aligned16(A))) return MOE_ERR_INVALID;
+  if (!aligned16(dB) || !aligned4(offsets)) return MOE_ERR_INVALID;
+  if (dB == dC || dB == A) return MOE_ERR_INVALID;
+  const moe_status_t space = grad_workspace(
+      ws, ws_bytes, moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, dt));
+  if (space != MOE_OK) return space;
+  if (rows == 0 && accumulate) return MOE_OK;
+  GradArgs a;
+  a.dC = dC, a.A = A, a.out = dB, a.offsets = offsets;
+  a.G = G, a.rows = rows, a.N = N, a.K = K, a.dt = dt, a.out_dt = b_dt;
+  a.accumulate = accumulate != 0;
+  return launched(launch_wgrad_simple(a, as_stream(stream)));
+}
+
+size_t moe_grad_norm_workspace_size(int n) {
+  return n < 0 || n > MOE_MAX_GRADS ? 0 : grad_norm_ws_bytes(n);
+}
+
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
+                           int n, float *norm, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  const moe_status_t list = grad_list(grads, sizes, dts, n);
+  if (list != MOE_OK) return list;
+  if (!aligned4(norm)) return MOE_ERR_INVALID;
+  if (ws_bytes < grad_norm_ws_bytes(n)) return MOE_ERR_WORKSPACE;
+  if (n > 0 && (!ws || reinterpret_cast<uintptr_t>(ws) % 8 != 0)) return MOE_ERR_INVALID;
+  static_assert(sizeof(moe_dtype_t) == sizeof(int), "types are passed on as ints");
+  return launched(launch_grad_norm(grads, sizes, reinterpret_cast<const int *>(dts), n, norm, ws,
+                                   as_stream(stream)));
+}
+
+moe_status_t moe_grad_clip(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
+                           int n, const float *norm, float max_norm, void *const *out,
+                           moe_stream_t stream) {
+  const moe_status_t list = grad_list(grads, sizes, dts, n);
+  if (list != MOE_OK) return list;
+  if (!aligned4(norm) || !(max_norm >= 0.f) || !(max_norm <= 3.4028234e38f)) return MOE_ERR_INVALID;
+  for (int i = 0; out && i < n; ++i)
+    if (sizes[i] > 0 && (!out[i] || reinterpret_cast<uintptr_t>(out[i]) % size_of(dts[i]) != 0))
+      return MOE_ERR_INVALID;
+  return launched(launch_grad_clip(grads, sizes, reinterpret_cast<const int *>(dts), n, norm,
+                                   max_norm, out, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -246,6 +246,59 @@ class MoELayer:
                                d_loss=d_loss, seq_offsets=seq_offsets, token_mask=token_mask)
         return d_logits
 
+    def backward(self, d_out, *, addend=None, weights=True, grad_dtype=None, grads=None):
+        """Gradients of the last forward from d_out [T][d]: a dict of dx [T][d],
+        d_topk_w [T][k] (for route_backward), and with weights=True the experts'
+        w_gate, w_up [G][dff][d] and w_down [G][d][dff], dense, of grad_dtype (the
+        weights' type, or fp32).  dx holds what came through the experts, plus
+        addend [T][d] if given (the router's part, d_logits times its weights, or
+        a residual's).  grads: a dict of w_gate, w_up and w_down to add the
+        weights' gradients to, as over several micro-batches.
+
+        bf16 or fp32 layers (not fp8, whose weights are quantised).  Only d_out, x
+        as permuted, Y and h are kept from the forward pass: the gate and up
+        products are computed again.  A forward of other tokens in between
+        replaces them."""
+        if self.fp8:
+            raise RuntimeError("backward needs bf16 or fp32 expert weights")
+        if self._T is None:
+            raise RuntimeError("backward needs a forward pass before it")
+        T, d, dff, G, ns = self._T, self.d, self.dff, self.G, self.n_shared
+        if d_out.shape != (T, d) or d_out.dtype != self.act_dtype:
+            raise ValueError("d_out must be %s [%d][%d], like the last forward's output"
+                             % (self.act_dtype, T, d))
+        dt, dev, f32 = self.act_dtype, self.device, torch.float32
+        rows = self.x_perm.shape[0]
+
+        def new(*shape, dtype=dt):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        out = {"d_topk_w": new(T, self.k, dtype=f32), "dx": new(T, d)}
+        dY = new(rows, d)
+        api.moe_combine_backward(d_out, self.y, self.flat_to_row, self.topk_w, dY,
+                                 out["d_topk_w"], n_shared=ns)
+        gate, up = new(rows, dff), new(rows, dff)
+        ws = new(max(16, api.moe_grouped_gemm_workspace_size(G, rows, dff, d, dt,
+                                                             api.MOE_EPI_NONE)),
+                 dtype=torch.uint8)
+        api.moe_grouped_gemm(self.x_perm, self.w_gate, gate, self.offsets, ws=ws)
+        api.moe_grouped_gemm(self.x_perm, self.w_up, up, self.offsets, ws=ws)
+        api.moe_grouped_gemm_dgrad_swiglu(dY, self.w_down, gate, up, gate, up, self.offsets)
+        # fp32 until the sum over a token's experts, like Y
+        dx_perm = new(rows, d, dtype=f32)
+        api.moe_grouped_gemm_dgrad(gate, self.w_gate, dx_perm, self.offsets, dC2=up,
+                                   B2=self.w_up)
+        api.moe_permute_backward(dx_perm, self.flat_to_row, out["dx"], self.k, n_shared=ns,
+                                 addend=addend)
+        if weights:
+            for name, dC, A, shape in (("w_down", dY, self.h, (G, d, dff)),
+                                       ("w_gate", gate, self.x_perm, (G, dff, d)),
+                                       ("w_up", up, self.x_perm, (G, dff, d))):
+                out[name] = new(*shape, dtype=grad_dtype or dt) if grads is None else grads[name]
+                api.moe_grouped_gemm_wgrad(dC, A, out[name], self.offsets,
+                                           accumulate=grads is not None)
+        return out
+
     @staticmethod
     def _agreed(balance, name, given):
         """What a balance_loss() result holds under name, or `given` where it
