@@ -60,6 +60,8 @@ __device__ __forceinline__ void slice_rows(int *r0, int *r1, int i, int n) {
 
 hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s);
+hipError_t launch_dgrad_bf16(const GradArgs &a, hipStream_t s);
+hipError_t launch_wgrad_bf16(const GradArgs &a, hipStream_t s);
 // out (+)= the slices' partial sums, in slice order
 hipError_t launch_wgrad_reduce(const GradArgs &a, hipStream_t s);
 

@@ -507,6 +507,14 @@ moe_status_t grad_workspace(const void *ws, size_t ws_bytes, size_t need) {
   return MOE_OK;
 }
 
+hipError_t launch_dgrad(const GradArgs &a, hipStream_t s) {
+  return a.dt == MOE_BF16 ? launch_dgrad_bf16(a, s) : launch_dgrad_simple(a, s);
+}
+
+hipError_t launch_wgrad(const GradArgs &a, hipStream_t s) {
+  return a.dt == MOE_BF16 ? launch_wgrad_bf16(a, s) : launch_wgrad_simple(a, s);
+}
+
 // the host arrays of a list of gradients
 moe_status_t grad_list(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
                        int n) {
@@ -581,7 +589,7 @@ moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *d
   GradArgs a;
   a.dC = dC, a.dC2 = dC2, a.B = B, a.B2 = B2, a.out = dA, a.offsets = offsets;
   a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb, a.dt = dt, a.out_dt = a_dt;
-  return launched(launch_dgrad_simple(a, as_stream(stream)));
+  return launched(launch_dgrad(a, as_stream(stream)));
 }
 
 moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dtype_t dt,
@@ -605,7 +613,7 @@ moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dt
   a.dC = dC, a.B = B, a.gate = gate, a.up = up, a.out = d_gate, a.out2 = d_up, a.h = h;
   a.offsets = offsets, a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb;
   a.dt = dt, a.out_dt = dt;
-  return launched(launch_dgrad_simple(a, as_stream(stream)));
+  return launched(launch_dgrad(a, as_stream(stream)));
 }
 
 size_t moe_grouped_gemm_wgrad_workspace_size(int G, int rows, int N, int K, moe_dtype_t dt) {
@@ -632,7 +640,7 @@ moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t d
   a.dC = dC, a.A = A, a.out = dB, a.offsets = offsets;
   a.G = G, a.rows = rows, a.N = N, a.K = K, a.dt = dt, a.out_dt = b_dt;
   a.accumulate = accumulate != 0;
-  return launched(launch_wgrad_simple(a, as_stream(stream)));
+  return launched(launch_wgrad(a, as_stream(stream)));
 }
 
 size_t moe_grad_norm_workspace_size(int n) {
