@@ -15,7 +15,9 @@ hipError_t launch_permute_backward(const void *dx_perm, int p_dt, const int32_t 
 
 // What the products' gradients work on.  dgrad: out [rows][K] = dC B (+ dC2
 // B2); with gate: SwiGLU's gradient, out = d_gate, out2 = d_up, h or null.
-// wgrad: out [G][N][K] (+)= dC^T A per group.
+// wgrad: out [G][N][K] (+)= dC^T A per group.  slices > 1: the sums are cut
+// along their terms (dgrad: N, wgrad: a group's rows), slice i's fp32 sums go
+// to part + i times the output's size, and a second launch adds them in order.
 struct GradArgs {
   const void *dC = nullptr, *dC2 = nullptr, *B = nullptr, *B2 = nullptr, *A = nullptr;
   const void *gate = nullptr, *up = nullptr;
@@ -24,7 +26,7 @@ struct GradArgs {
   int G = 0, rows = 0, N = 0, K = 0, ldb = 0;
   int dt = 0, out_dt = 0;
   int accumulate = 0;
-  float *part = nullptr;  // wgrad: partial sums [slice][G][N][K], or null
+  float *part = nullptr;
   int slices = 1;
 };
 
@@ -62,8 +64,20 @@ hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s);
 hipError_t launch_dgrad_bf16(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_bf16(const GradArgs &a, hipStream_t s);
-// out (+)= the slices' partial sums, in slice order
+// the slices' sums added in slice order and stored as the launch without slices
+// would (dgrad: the rows of all groups)
+hipError_t launch_dgrad_reduce(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_reduce(const GradArgs &a, hipStream_t s);
+
+// Row tiles of BM rows that groups can have: at most one partly filled tile for
+// each group with a row.
+inline int row_tiles(int rows, int G, int BM) { return rows / BM + (G < rows ? G : rows); }
+
+// Slices of the sums, so that few tiles with long sums fill the chip.  A slice
+// is worth its share of a second launch (4 us) from about eight stages or
+// chunks on; it keeps at least four.
+int dgrad_slices(int G, int rows, int N, int K, int dt, int cus);
+int wgrad_slices(int G, int rows, int N, int K, int dt, int cus);
 
 size_t grad_norm_ws_bytes(int n);
 hipError_t launch_grad_norm(const void *const *grads, const int64_t *sizes, const int *dts, int n,

@@ -113,7 +113,8 @@ __device__ __forceinline__ void run_sum(f32x16 (&acc)[MI][NB], const OpA &oa, co
 // One dgrad tile of at most BM rows and 256 columns.  SHORT: N is less than a
 // stage.
 template <int BM, bool SHORT, class Out>
-__device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, const Ring23 &ring) {
+__device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, int slice,
+                                           const Ring23 &ring) {
   typedef AlongOperand<BM> OpA;
   typedef CrossOperand<256, 64> OpB;
   constexpr int IA = OpA::IL, IB = OpB::IL;
@@ -134,13 +135,17 @@ __device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, 
   }
   const Span<64> span(a.N);
   const size_t first_a = (size_t)tile.m0 * a.N, first_b = (size_t)tile.g * a.N * a.ldb + k0;
-  // both products in one run of stages, or, where each ends inside a stage, one
-  // after the other
-  const int parts = a.dC2 && span.back ? 2 : 1;
-  const int stages = a.dC2 && !span.back ? 2 * span.stages : span.stages;
+  // this slice's stages of one product; both products in one run of stages, or,
+  // where each ends inside a stage or is cut, one after the other
+  const int per = (span.stages + a.slices - 1) / a.slices, st0 = slice * per;
+  const int count = min(per, span.stages - st0);
+  const int back = st0 + count == span.stages ? span.back : 0;
+  const bool joined = a.dC2 && !span.back && a.slices == 1;
+  const int parts = a.dC2 && !joined ? 2 : 1;
+  const int stages = joined ? 2 * count : count;
   int part = 0;
   auto issue_a = [&](int st, u32x4 *slot) {
-    st = min(st, stages - 1);
+    st = min(st, stages - 1) + st0;
     const bool second = part || st >= span.stages;
     st -= second && !part ? span.stages : 0;
     const uint16_t *const p = static_cast<const uint16_t *>(second ? a.dC2 : a.dC) + first_a +
@@ -155,7 +160,7 @@ __device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, 
     }
   };
   auto issue_b = [&](int st, u32x4 *slot) {
-    st = min(st, stages - 1);
+    st = min(st, stages - 1) + st0;
     const bool second = part || st >= span.stages;
     st -= second && !part ? span.stages : 0;
     const uint16_t *const p = static_cast<const uint16_t *>(second ? a.B2 : a.B) + first_b +
@@ -178,10 +183,10 @@ __device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, 
 #pragma unroll
     for (int j = 0; j < OpB::NB; ++j) acc[i][j] = f32x16{};
   for (; part < parts; ++part) {
-    run_sum(acc, oa, ob, stages, span.back, ring, issue_a, issue_b);
+    run_sum(acc, oa, ob, stages, back, ring, issue_a, issue_b);
     stage_barrier();  // every wave is done reading the ring
   }
-  const Out out = {a, tile.m0, tile.mend, k0};
+  const Out out = {a, tile.m0, tile.mend, k0, (size_t)slice * a.rows * a.K};
   u32x4 *const mine = wv == 0 ? ring.a0 : wv == 1 ? ring.a1 : wv == 2 ? ring.b0 : ring.b1;
   if (tile.mend - tile.m0 == BM && k0 + 256 <= a.K) each_piece<true, 64>(acc, mine, out);
   else each_piece<false, 64>(acc, mine, out);
@@ -199,6 +204,7 @@ struct DgradOut {
   static constexpr int COLS = OUT_F32 ? 4 : 8, DEPTH = 2;
   const GradArgs &a;
   int m0, mend, k0;
+  size_t first;  // where the slice's outputs begin
   struct Held {
     u32x4 gate, up;
   };
@@ -217,7 +223,7 @@ struct DgradOut {
   template <bool FULL>
   __device__ __forceinline__ void finish(int r, int c, const Held &x, const float *v) const {
     if (!FULL && (m0 + r >= mend || k0 + c >= a.K)) return;
-    const size_t at = (size_t)(m0 + r) * a.K + k0 + c;
+    const size_t at = first + (size_t)(m0 + r) * a.K + k0 + c;
     if constexpr (SWIGLU) {
       float z[8], u[8], dg[8], du[8], h[8];
       widen8(x.gate, z);
@@ -245,26 +251,33 @@ __global__ __launch_bounds__(NW * 64, 1) void dgrad_kernel(const GradArgs a, int
   constexpr int SLOT = pieces(256, 64);
   __shared__ u32x4 a0[SLOT], a1[SLOT], b0[SLOT], b1[SLOT], b2[SLOT];
   const Ring23 ring = {a0, a1, b0, b1, b2};
+  const int w = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
   // (the scheduler's result lies in a slot that the ring fills later)
   const Sched sc = sched_lookup(a.offsets, a.G, a.rows, 256, nt, kTileChunk, false,
                                 reinterpret_cast<int *>(b2),
-                                [](int total) { return tile_of_workgroup(blockIdx.x, total); });
+                                [w](int total) { return tile_of_workgroup(w, total); });
   if (sc.L < 0) return;
   const Tile tile = sc.tile;
   typedef DgradOut<SWIGLU, OUT_F32, STREAM> Out;
   const int rows = tile.mend - tile.m0;
-  if (rows > 128) dgrad_tile<256, SHORT, Out>(a, tile, ring);
-  else if (rows > 64) dgrad_tile<128, SHORT, Out>(a, tile, ring);
-  else dgrad_tile<64, SHORT, Out>(a, tile, ring);
+  if (rows > 128) dgrad_tile<256, SHORT, Out>(a, tile, slice, ring);
+  else if (rows > 64) dgrad_tile<128, SHORT, Out>(a, tile, slice, ring);
+  else dgrad_tile<64, SHORT, Out>(a, tile, slice, ring);
 }
 
 }  // namespace
 
-hipError_t launch_dgrad_bf16(const GradArgs &a, hipStream_t s) {
+hipError_t launch_dgrad_bf16(const GradArgs &args, hipStream_t s) {
+  GradArgs a = args;
+  if (a.slices > 1) {
+    a.out = a.part;
+    a.out_dt = MOE_F32;
+    a.gate = nullptr;
+  }
   const int nt = (a.K + 255) / 256;
-  const dim3 grid((unsigned)(host_row_tile_bound(a.rows, a.G, 256) * (long long)nt)), block(NW * 64);
+  const dim3 grid((unsigned)(row_tiles(a.rows, a.G, 256) * (long long)nt * a.slices)), block(NW * 64);
   const bool brief = a.N < 64;
-  const bool stream = streams(a.rows, a.K * (a.out_dt == MOE_F32 ? 4 : 2), a.gate ? 2 + (a.h != nullptr) : 1);
+  const bool stream = a.slices == 1 && streams(a.rows, a.K * (a.out_dt == MOE_F32 ? 4 : 2), a.gate ? 2 + (a.h != nullptr) : 1);
 #define MOE_LAUNCH(SW, F32)                                                                          \
   if (brief) hipLaunchKernelGGL((dgrad_kernel<SW, F32, false, true>), grid, block, 0, s, a, nt);     \
   else if (stream) hipLaunchKernelGGL((dgrad_kernel<SW, F32, true, false>), grid, block, 0, s, a, nt); \

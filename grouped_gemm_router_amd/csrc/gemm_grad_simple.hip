@@ -108,15 +108,19 @@ template <int ES, int OS, bool SWIGLU>
 __global__ __launch_bounds__(256) void dgrad_simple_kernel(const GradArgs a, int nt) {
   __shared__ Shared s;
   __shared__ int s_x[8];
+  const int w = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
   const Sched sc = sched_lookup(a.offsets, a.G, a.rows, BT, nt, kTileChunk, false, s_x,
-                                [](int total) { return tile_of_workgroup(blockIdx.x, total); });
+                                [w](int total) { return tile_of_workgroup(w, total); });
   if (sc.L < 0) return;
   const Tile tile = sc.tile;
   const int t = threadIdx.x;
   const int row = tile.m0 + t / 4, col = tile.nt * BT + (t % 8) * 8;
   // the second product's terms follow the first's, from a whole step on
   const int span = (a.N + KC - 1) / KC * KC;
-  const f32x16 acc = product<true>(s, a.dC2 ? 2 * span : span, [&](int k0, float *x, float *y) {
+  const int terms = a.dC2 ? 2 * span : span;
+  const int per = (terms / KC + a.slices - 1) / a.slices * KC, first = slice * per;
+  const f32x16 acc = product<true>(s, min(per, terms - first), [&](int k0, float *x, float *y) {
+    k0 += first;
     const bool second = k0 >= span;
     const int n0 = second ? k0 - span : k0;
     const int na = n0 + (t % 4) * 8, nb = n0 + t / 8;
@@ -130,7 +134,7 @@ __global__ __launch_bounds__(256) void dgrad_simple_kernel(const GradArgs a, int
   each_output(acc, [&](int r, int c, float v) {
     const int m = tile.m0 + r, k = tile.nt * BT + c;
     if (m >= tile.mend || k >= a.K) return;
-    const size_t at = (size_t)m * a.K + k;
+    const size_t at = ((size_t)slice * a.rows + m) * a.K + k;
     if constexpr (SWIGLU) {
       const float g = get<ES>(a.gate, at), u = get<ES>(a.up, at);
       const float sig = 1.f / (1.f + expf(-g));
@@ -155,7 +159,7 @@ __global__ __launch_bounds__(256) void wgrad_simple_kernel(const GradArgs a, int
   const int g = w % a.G, slice = w / a.G;
   group_rows(a.offsets, a.rows, g, s_rows);
   int r0 = s_rows[0], r1 = s_rows[1];
-  if (a.part) slice_rows(&r0, &r1, slice, a.slices);
+  if (a.slices > 1) slice_rows(&r0, &r1, slice, a.slices);
   const int t = threadIdx.x;
   const int ca = n0 + (t % 8) * 8, cb = k0 + (t % 8) * 8;
   const f32x16 acc = product<false>(s, r1 - r0, [&](int k, float *x, float *y) {
@@ -168,37 +172,94 @@ __global__ __launch_bounds__(256) void wgrad_simple_kernel(const GradArgs a, int
   each_output(acc, [&](int r, int c, float v) {
     const int n = n0 + r, k = k0 + c;
     if (n >= a.N || k >= a.K) return;
-    const size_t at = ((size_t)g * a.N + n) * a.K + k;
-    if (a.part) a.part[(size_t)slice * a.G * a.N * a.K + at] = v;
-    else put<OS>(a.out, at, a.accumulate ? v + get<OS>(a.out, at) : v);
+    const size_t at = (((size_t)slice * a.G + g) * a.N + n) * a.K + k;
+    put<OS>(a.out, at, a.accumulate ? v + get<OS>(a.out, at) : v);
   });
 }
 
-// out (+)= the sum of the slices' partial sums, in slice order; 8 outputs a
-// thread and step
+// the slices' sums of 8 outputs from e on, in slice order
+__device__ __forceinline__ void sum8(const GradArgs &a, size_t all, size_t e, float sum[8]) {
+  load8<4>(a.part, e, sum);
+  float v[8];
+  for (int i = 1; i < a.slices; ++i) {
+    load8<4>(a.part, (size_t)i * all + e, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] += v[q];
+  }
+}
+
+template <int OS>
+__device__ __forceinline__ void store8(void *p, size_t e, const float v[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) put<OS>(p, e + q, v[q]);
+}
+
 template <int OS>
 __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const GradArgs a) {
   const size_t all = (size_t)a.G * a.N * a.K;
   for (size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; e < all;
        e += (size_t)gridDim.x * 256 * 8) {
     float sum[8], v[8];
-    load8<4>(a.part, e, sum);
-    for (int i = 1; i < a.slices; ++i) {
-      load8<4>(a.part, (size_t)i * all + e, v);
+    sum8(a, all, e, sum);
+    if (a.accumulate) {
+      load8<OS>(a.out, e, v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) sum[q] += v[q];
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      put<OS>(a.out, e + q, a.accumulate ? sum[q] + get<OS>(a.out, e + q) : sum[q]);
+    store8<OS>(a.out, e, sum);
   }
+}
+
+// ES: element size of the operands; rows outside every group are left alone
+template <int ES, int OS, bool SWIGLU>
+__global__ __launch_bounds__(256) void dgrad_reduce_kernel(const GradArgs a) {
+  __shared__ int s_last[2], s_first[2];
+  group_rows(a.offsets, a.rows, a.G - 1, s_last);
+  group_rows(a.offsets, a.rows, 0, s_first);
+  const size_t all = (size_t)a.rows * a.K;
+  const size_t begin = (size_t)s_first[0] * a.K, end = (size_t)s_last[1] * a.K;
+  for (size_t e = begin + ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; e < end;
+       e += (size_t)gridDim.x * 256 * 8) {
+    float v[8];
+    sum8(a, all, e, v);
+    if constexpr (SWIGLU) {
+      float g[8], u[8], dg[8], du[8], h[8];
+      load8<ES>(a.gate, e, g);
+      load8<ES>(a.up, e, u);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float s = 1.f / (1.f + expf(-g[q]));
+        dg[q] = v[q] * u[q] * s * (1.f + g[q] * (1.f - s));
+        du[q] = v[q] * g[q] * s;
+        h[q] = g[q] * s * u[q];
+      }
+      store8<OS>(a.out, e, dg);
+      store8<OS>(a.out2, e, du);
+      if (a.h) store8<OS>(a.h, e, h);
+    } else {
+      store8<OS>(a.out, e, v);
+    }
+  }
+}
+
+// the arguments of the launch that writes slices: plain fp32 sums
+GradArgs sliced(const GradArgs &args) {
+  GradArgs a = args;
+  if (a.slices > 1) {
+    a.out = a.part;
+    a.out_dt = MOE_F32;
+    a.gate = nullptr;
+    a.accumulate = 0;
+  }
+  return a;
 }
 
 }  // namespace
 
-hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s) {
+hipError_t launch_dgrad_simple(const GradArgs &args, hipStream_t s) {
+  const GradArgs a = sliced(args);
   const int nt = (a.K + BT - 1) / BT;
-  const dim3 grid((unsigned)(host_row_tile_bound(a.rows, a.G, BT) * (long long)nt)), block(256);
+  const dim3 grid((unsigned)(row_tiles(a.rows, a.G, BT) * (long long)nt * a.slices)), block(256);
 #define MOE_LAUNCH(ES, OS, SW) \
   hipLaunchKernelGGL((dgrad_simple_kernel<ES, OS, SW>), grid, block, 0, s, a, nt)
   if (a.gate) {
@@ -212,7 +273,8 @@ hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s) {
+hipError_t launch_wgrad_simple(const GradArgs &args, hipStream_t s) {
+  const GradArgs a = sliced(args);
   const int nt = (a.N + BT - 1) / BT, kt = (a.K + BT - 1) / BT;
   const dim3 grid((unsigned)((long long)a.slices * a.G * nt * kt)), block(256);
 #define MOE_LAUNCH(ES, OS) \
@@ -224,10 +286,60 @@ hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+namespace {
+
+// 8 outputs a thread, at most 4096 workgroups
+dim3 reduce_grid(size_t outputs) {
+  const size_t groups = (outputs / 8 + 255) / 256;
+  return dim3((unsigned)(groups < 4096 ? groups : 4096));
+}
+
+}  // namespace
+
 hipError_t launch_wgrad_reduce(const GradArgs &a, hipStream_t s) {
-  const size_t groups = ((size_t)a.G * a.N * a.K / 8 + 255) / 256;
-  const dim3 grid((unsigned)(groups < 4096 ? groups : 4096)), block(256);
+  const dim3 grid = reduce_grid((size_t)a.G * a.N * a.K), block(256);
   if (a.out_dt == MOE_BF16) hipLaunchKernelGGL(wgrad_reduce_kernel<2>, grid, block, 0, s, a);
   else hipLaunchKernelGGL(wgrad_reduce_kernel<4>, grid, block, 0, s, a);
   return hipGetLastError();
+}
+
+hipError_t launch_dgrad_reduce(const GradArgs &a, hipStream_t s) {
+  const dim3 grid = reduce_grid((size_t)a.rows * a.K), block(256);
+#define MOE_LAUNCH(ES, OS, SW) \
+  hipLaunchKernelGGL((dgrad_reduce_kernel<ES, OS, SW>), grid, block, 0, s, a)
+  if (a.gate) {
+    if (a.dt == MOE_BF16) MOE_LAUNCH(2, 2, true); else MOE_LAUNCH(4, 4, true);
+  } else if (a.out_dt == MOE_BF16) {
+    MOE_LAUNCH(2, 2, false);
+  } else {
+    MOE_LAUNCH(4, 4, false);
+  }
+#undef MOE_LAUNCH
+  return hipGetLastError();
+}
+
+int dgrad_slices(int G, int rows, int N, int K, int dt, int cus) {
+  // the bf16 kernel's tiles are 256 x 256 outputs with stages of 64 terms, one
+  // workgroup a CU; this file's 64 x 64 with steps of 32 terms, four a CU
+  const bool bf16 = dt == MOE_BF16;
+  const int side = bf16 ? 256 : BT, steps = (N + (bf16 ? 64 : KC) - 1) / (bf16 ? 64 : KC);
+  const long long tiles = (long long)row_tiles(rows, G, side) * ((K + side - 1) / side);
+  const long long room = (long long)cus * (bf16 ? 1 : 4);
+  if (tiles == 0 || 2 * tiles > room || steps < 8) return 1;
+  int n = (int)(room / tiles < steps / 4 ? room / tiles : steps / 4);
+  const int per = (steps + n - 1) / n;
+  return (steps + per - 1) / per;  // (none of them empty)
+}
+
+int wgrad_slices(int G, int rows, int N, int K, int dt, int cus) {
+  // bf16: tiles of 128 x 256 weights with stages of 32 rows, two workgroups a CU
+  const bool bf16 = dt == MOE_BF16;
+  const long long tn = bf16 ? 128 : BT, tk = bf16 ? 256 : BT;
+  const long long tiles = (N + tn - 1) / tn * ((K + tk - 1) / tk) * G;
+  const long long room = (long long)cus * (bf16 ? 2 : 4);
+  const int steps = rows / G / 32;  // of an average group
+  // (two or three slices gain less than their sums cost: 36 groups of 847 rows,
+  // 40 x 1560 weights in two slices 32 -> 40 us)
+  if (4 * tiles > room || steps < 8) return 1;
+  return (int)(room / tiles < steps / 4 ? room / tiles : steps / 4);
 }

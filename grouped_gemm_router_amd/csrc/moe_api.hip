@@ -507,13 +507,24 @@ moe_status_t grad_workspace(const void *ws, size_t ws_bytes, size_t need) {
   return MOE_OK;
 }
 
+// (256: where no device can be asked, as for a size query without one)
+int grad_cus() {
+  const int n = current_device_cus();
+  return n > 0 ? n : 256;
+}
+
 hipError_t launch_dgrad(const GradArgs &a, hipStream_t s) {
-  return a.dt == MOE_BF16 ? launch_dgrad_bf16(a, s) : launch_dgrad_simple(a, s);
+  const hipError_t e = a.dt == MOE_BF16 ? launch_dgrad_bf16(a, s) : launch_dgrad_simple(a, s);
+  return e == hipSuccess && a.slices > 1 ? launch_dgrad_reduce(a, s) : e;
 }
 
 hipError_t launch_wgrad(const GradArgs &a, hipStream_t s) {
-  return a.dt == MOE_BF16 ? launch_wgrad_bf16(a, s) : launch_wgrad_simple(a, s);
+  const hipError_t e = a.dt == MOE_BF16 ? launch_wgrad_bf16(a, s) : launch_wgrad_simple(a, s);
+  return e == hipSuccess && a.slices > 1 ? launch_wgrad_reduce(a, s) : e;
 }
+
+// bytes of n slices of `outputs` fp32 sums (none for one slice)
+size_t slice_bytes(int n, size_t outputs) { return n > 1 ? n * outputs * sizeof(float) : 0; }
 
 // the host arrays of a list of gradients
 moe_status_t grad_list(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
@@ -566,8 +577,9 @@ moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
 }
 
 size_t moe_grouped_gemm_dgrad_workspace_size(int G, int rows, int N, int K, moe_dtype_t dt) {
-  (void)G, (void)rows, (void)N, (void)K, (void)dt;
-  return 0;
+  int ldb = 0;
+  if (grad_sizes(G, rows, N, K, &ldb, dt) != MOE_OK) return 0;
+  return slice_bytes(dgrad_slices(G, rows, N, K, dt, grad_cus()), (size_t)rows * K);
 }
 
 moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *dC2,
@@ -589,6 +601,7 @@ moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *d
   GradArgs a;
   a.dC = dC, a.dC2 = dC2, a.B = B, a.B2 = B2, a.out = dA, a.offsets = offsets;
   a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb, a.dt = dt, a.out_dt = a_dt;
+  a.slices = dgrad_slices(G, rows, N, K, dt, grad_cus()), a.part = static_cast<float *>(ws);
   return launched(launch_dgrad(a, as_stream(stream)));
 }
 
@@ -613,12 +626,14 @@ moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dt
   a.dC = dC, a.B = B, a.gate = gate, a.up = up, a.out = d_gate, a.out2 = d_up, a.h = h;
   a.offsets = offsets, a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb;
   a.dt = dt, a.out_dt = dt;
+  a.slices = dgrad_slices(G, rows, N, K, dt, grad_cus()), a.part = static_cast<float *>(ws);
   return launched(launch_dgrad(a, as_stream(stream)));
 }
 
 size_t moe_grouped_gemm_wgrad_workspace_size(int G, int rows, int N, int K, moe_dtype_t dt) {
-  (void)G, (void)rows, (void)N, (void)K, (void)dt;
-  return 0;
+  int ldb = 0;
+  if (grad_sizes(G, rows, N, K, &ldb, dt) != MOE_OK) return 0;
+  return slice_bytes(wgrad_slices(G, rows, N, K, dt, grad_cus()), (size_t)G * N * K);
 }
 
 moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t dt, void *dB,
@@ -640,6 +655,7 @@ moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t d
   a.dC = dC, a.A = A, a.out = dB, a.offsets = offsets;
   a.G = G, a.rows = rows, a.N = N, a.K = K, a.dt = dt, a.out_dt = b_dt;
   a.accumulate = accumulate != 0;
+  a.slices = wgrad_slices(G, rows, N, K, dt, grad_cus()), a.part = static_cast<float *>(ws);
   return launched(launch_wgrad(a, as_stream(stream)));
 }
 
