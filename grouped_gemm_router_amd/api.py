@@ -8,7 +8,10 @@ it has not been built (``python -m grouped_gemm_router_amd.build``).
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
+import itertools
+import operator
 import os
 import threading
 
@@ -154,11 +157,12 @@ def _deferring() -> bool:
     return getattr(_defer, "on", False)
 
 
-def _invoke(fn: str, cfn, *args):
+def _invoke(fn: str, cfn, *args, keep=None):
     """Call the library entry cfn with marshalled args and check the status;
-    inside deferred(), return that call as a thunk instead of making it."""
+    inside deferred(), return that call as a thunk instead of making it, which
+    holds `keep`, host memory that args point to."""
     if _deferring():
-        def call():
+        def call(keep=keep):
             status = cfn(*args)
             if status != MOE_OK:
                 raise MoEError(fn, status)
@@ -658,20 +662,25 @@ def _act(t, name) -> int:
 
 def _experts(B, name, dtype, N, device):
     """(pointer, G, K, row pitch) of [G][N][K] weights whose rows may be padded."""
-    if not isinstance(B, torch.Tensor) or B.dim() != 3 or B.dtype != dtype:
+    if not isinstance(B, torch.Tensor) or B.dtype is not dtype or B.dim() != 3:
         raise TypeError("%s must be a [G][N][K] %s tensor" % (name, dtype))
-    if B.shape[1] != N:
+    G, rows, K = B.shape
+    if rows != N:
         raise ValueError("%s must have %d rows an expert, got %s" % (name, N, list(B.shape)))
     if B.get_device() != device:
         raise ValueError("%s must be on GPU %d, like the other tensors" % (name, device))
-    p, _, ldb = _weights(B)
-    return p, B.shape[0], B.shape[2], ldb
+    return B.data_ptr(), G, K, K if B.is_contiguous() else _weights(B)[2]
 
 
-def _own_workspace(ws, size, device, stream):
-    """(pointer, bytes) of a workspace that may be of size 0."""
-    if size == 0 and ws is None:
-        return None, 0, None
+def _own_workspace(ws, device, stream, query, *sizes):
+    """(pointer, bytes, tensor) of a workspace: ws, or a new one of the size that
+    query(*sizes) says, which may be 0."""
+    if ws is None:
+        size = query(*sizes)
+        if size == 0:
+            return None, 0, None
+    else:
+        size = 0
     ws, ws_bytes = _workspace(ws, size, device, stream)
     return ws.data_ptr(), ws_bytes, ws
 
@@ -697,8 +706,8 @@ def moe_grouped_gemm_dgrad(dC, B, dA, offsets, *, dC2=None, B2=None, ws=None, st
             raise ValueError("B2 must have B's shape and strides")
     if dA.dtype not in (dt, torch.float32):
         raise TypeError("dA must be %s or %s, got %s" % (dt, torch.float32, dA.dtype))
-    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt), dev,
-                                stream)
+    pw, wb, ws = _own_workspace(ws, dev, stream, moe_grouped_gemm_dgrad_workspace_size, G, rows, N,
+                                K, dt)
     return _invoke("moe_grouped_gemm_dgrad", lib.moe_grouped_gemm_dgrad,
                    _arg(dC, "dC", dt, (rows, N), dev), p,
                    _arg(dC2, "dC2", dt, (rows, N), dev), p2, _act(dC, "dC"),
@@ -716,8 +725,8 @@ def moe_grouped_gemm_dgrad_swiglu(dC, B, gate, up, d_gate, d_up, offsets, *, h=N
     dt = dC.dtype
     dev = _gpu(dC, "dC")
     p, G, K, ldb = _experts(B, "B", dt, N, dev)
-    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt), dev,
-                                stream)
+    pw, wb, ws = _own_workspace(ws, dev, stream, moe_grouped_gemm_dgrad_workspace_size, G, rows, N,
+                                K, dt)
     of = (rows, K)
     return _invoke("moe_grouped_gemm_dgrad_swiglu", lib.moe_grouped_gemm_dgrad_swiglu,
                    _arg(dC, "dC", dt, (rows, N), dev), p, _act(dC, "dC"),
@@ -745,8 +754,8 @@ def moe_grouped_gemm_wgrad(dC, A, dB, offsets, *, accumulate=False, ws=None, str
     dev = _gpu(dB, "dB")
     if dB.dtype not in (dt, torch.float32):
         raise TypeError("dB must be %s or %s, got %s" % (dt, torch.float32, dB.dtype))
-    pw, wb, ws = _own_workspace(ws, moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, dt), dev,
-                                stream)
+    pw, wb, ws = _own_workspace(ws, dev, stream, moe_grouped_gemm_wgrad_workspace_size, G, rows, N,
+                                K, dt)
     return _invoke("moe_grouped_gemm_wgrad", lib.moe_grouped_gemm_wgrad,
                    _arg(dC, "dC", dt, (rows, N), dev), _arg(A, "A", dt, (rows, K), dev),
                    _act(dC, "dC"), _arg(dB, "dB", dB.dtype, (G, N, K), dev), _act(dB, "dB"),
@@ -754,17 +763,30 @@ def moe_grouped_gemm_wgrad(dC, A, dB, offsets, *, accumulate=False, ws=None, str
                    1 if accumulate else 0, pw, wb, _raw_stream(stream, dev))
 
 
+_dtype_of = operator.attrgetter("dtype")
+_ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _grads(grads, name, device):
     """Host arrays (pointers, sizes, types) of a list of gradients."""
-    n = len(grads)
-    ptrs, sizes, dts = (C.c_void_p * n)(), (C.c_int64 * n)(), (C.c_int * n)()
-    for i, t in enumerate(grads):
-        if t.get_device() != device:
-            raise ValueError("%s[%d] must be on GPU %d, like norm" % (name, i, device))
-        if not t.is_contiguous():
-            raise ValueError("%s[%d] must be contiguous" % (name, i))
-        ptrs[i], sizes[i], dts[i] = t.data_ptr(), t.numel(), _act(t, name)
-    return ptrs, sizes, dts
+    # (whole lists through map: half the time of a loop over 100 tensors)
+    T = torch.Tensor
+    if not all(map(isinstance, grads, itertools.repeat(T))):
+        raise TypeError("%s must hold torch.Tensors" % name)
+    if grads and set(map(T.get_device, grads)) != {device}:
+        raise ValueError("%s must be on GPU %d, like norm" % (name, device))
+    if not all(map(T.is_contiguous, grads)):
+        raise ValueError("%s must be contiguous" % name)
+    try:
+        dts = array.array("i", [_ACT[t] for t in map(_dtype_of, grads)])
+    except KeyError as e:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, e.args[0])) from None
+    return array.array("Q", map(T.data_ptr, grads)), array.array("q", map(T.numel, grads)), dts
+
+
+def _at(a):
+    """Address of an array's first element."""
+    return a.buffer_info()[0]
 
 
 def moe_grad_norm_workspace_size(n: int) -> int:
@@ -777,10 +799,11 @@ def moe_grad_norm(grads, norm, *, ws=None, stream=None):
     moe_grad_norm_workspace_size(len(grads)) bytes; when None, one is allocated
     here for this call."""
     dev = _gpu(norm, "norm")
-    ptrs, sizes, dts = _grads(grads, "grads", dev)
-    pw, wb, ws = _own_workspace(ws, moe_grad_norm_workspace_size(len(grads)), dev, stream)
-    return _invoke("moe_grad_norm", lib.moe_grad_norm, ptrs, sizes, dts, len(grads),
-                   _arg(norm, "norm", torch.float32, (1,), dev), pw, wb, _raw_stream(stream, dev))
+    host = ptrs, sizes, dts = _grads(grads, "grads", dev)
+    pw, wb, ws = _own_workspace(ws, dev, stream, moe_grad_norm_workspace_size, len(grads))
+    return _invoke("moe_grad_norm", lib.moe_grad_norm, _at(ptrs), _at(sizes), _at(dts), len(grads),
+                   _arg(norm, "norm", torch.float32, (1,), dev), pw, wb, _raw_stream(stream, dev),
+                   keep=host)
 
 
 def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
@@ -792,8 +815,9 @@ def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
     outs = None
     if out is not None:
         outs, osizes, odts = _grads(out, "out", dev)
-        if osizes[:] != sizes[:] or odts[:] != dts[:]:
+        if osizes != sizes or odts != dts:
             raise ValueError("out must have the gradients' sizes and types")
-    return _invoke("moe_grad_clip", lib.moe_grad_clip, ptrs, sizes, dts, len(grads),
-                   _arg(norm, "norm", torch.float32, (1,), dev), float(max_norm), outs,
-                   _raw_stream(stream, dev))
+    return _invoke("moe_grad_clip", lib.moe_grad_clip, _at(ptrs), _at(sizes), _at(dts), len(grads),
+                   _arg(norm, "norm", torch.float32, (1,), dev), float(max_norm),
+                   None if outs is None else _at(outs), _raw_stream(stream, dev),
+                   keep=(ptrs, sizes, dts, outs))

@@ -183,3 +183,25 @@ def test_the_same_bits_again_on_a_stream_and_in_a_graph():
         a.moe_grad_norm(grads, eager)
         torch.cuda.synchronize()
         assert torch.equal(norm, eager) and float(norm) == float(want[0]) * 2 ** (k + 1)
+
+
+def test_a_deferred_step():
+    """Calls marshalled once: their host arrays live as long as the thunk, and
+    they read what the gradients hold then."""
+    import gc
+    grads, _ = make([4000, 9, 70001], [F32, BF], 1)
+    a = api()
+    norm = torch.empty((1,), device=DEV)
+    ws = torch.empty((a.moe_grad_norm_workspace_size(3),), dtype=torch.uint8, device=DEV)
+    out = [torch.empty_like(g) for g in grads]
+    calls = [a.deferred(a.moe_grad_norm, grads, norm, ws=ws),
+             a.deferred(a.moe_grad_clip, grads, norm, 0.5, out=out)]
+    gc.collect()
+    for _ in range(2):
+        for g in grads:
+            g.mul_(3.0)
+        for c in calls:
+            c()
+        want = norm64(grads)
+        close(norm, want, 1)
+        assert norm64(out) == pytest.approx(0.5, rel=0.01)
