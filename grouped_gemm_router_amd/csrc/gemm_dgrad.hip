@@ -55,8 +55,8 @@ struct Ring23 {
   interleave<MI * NB, OpA::READS + OpB::READS, loads>();    \
   __builtin_amdgcn_sched_barrier(0);
 #define MOE_STAGE(d, sa, sb, na, nb, pb, check)             \
-  MOE_STEP(sa, sb, 1, f0, f1, OpB::IL, issue_b((d) + 2, r.pb)) \
-  MOE_STEP(sa, sb, 2, f1, f0, 0, )                          \
+  MOE_STEP(sa, sb, 1, f0, f1, OpB::IL / 2, issue_b((d) + 2, r.pb, 0)) \
+  MOE_STEP(sa, sb, 2, f1, f0, OpB::IL / 2, issue_b((d) + 2, r.pb, 1)) \
   MOE_STEP(sa, sb, 3, f0, f1, 0, )                          \
   wait_vmcnt_lgkm0<OpB::IL>();                              \
   stage_barrier();                                          \
@@ -66,9 +66,11 @@ template <int MI, int NB, class OpA, class OpB, class IssueA, class IssueB>
 __device__ __forceinline__ void run_sum(f32x16 (&acc)[MI][NB], const OpA &oa, const OpB &ob,
                                         int stages, int z, const Ring23 &r, IssueA issue_a,
                                         IssueB issue_b) {
-  issue_b(0, r.b0);
+  issue_b(0, r.b0, 0);
+  issue_b(0, r.b0, 1);
   issue_a(0, r.a0);
-  issue_b(1, r.b1);
+  issue_b(1, r.b1, 0);
+  issue_b(1, r.b1, 1);
   issue_a(1, r.a1);
   wait_vmcnt<OpA::IL + OpB::IL>();
   stage_barrier();
@@ -159,14 +161,15 @@ __device__ __forceinline__ void dgrad_tile(const GradArgs &a, const Tile &tile, 
       else load_lds(p, at_a[i], to);
     }
   };
-  auto issue_b = [&](int st, u32x4 *slot) {
+  auto issue_b = [&](int st, u32x4 *slot, int half) {
     st = min(st, stages - 1) + st0;
     const bool second = part || st >= span.stages;
     st -= second && !part ? span.stages : 0;
     const uint16_t *const p = static_cast<const uint16_t *>(second ? a.B2 : a.B) + first_b +
                               (size_t)(SHORT ? 0 : span.first(st)) * a.ldb;
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
+    for (int j = 0; j < IB / 2; ++j) {
+      const int i = half * (IB / 2) + j;
       u32x4 *const to = slot + (wv * IB + i) * 64;
       if constexpr (SHORT)
         load_lds(or_zeros(OpB::load_row(wv, i, lane) < a.N, p + at_b[i] / 2), 0, to);

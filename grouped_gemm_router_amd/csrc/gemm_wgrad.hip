@@ -15,51 +15,55 @@ struct Ring3 {
 };
 constexpr int SB = pieces(128, 32);  // where the second operand begins in a slot
 
-#define MOE_HALF_0(cur)                                \
+#define MOE_HALF_0(s, cur, prv)                        \
+  issue_b((s) + 2, r.prv + SB);                        \
   read_frag(f1, oa, ob, r.cur, r.cur + SB, 1);         \
   mfma_frag(acc, f0);                                  \
-  interleave<MI * NB, OpA::READS + OpB::READS, 0>();   \
+  interleave<MI * NB, OpA::READS + OpB::READS, OpB::IL>(); \
   __builtin_amdgcn_sched_barrier(0);                   \
   wait_vmcnt_lgkm0<IL>();                              \
   stage_barrier();
 #define MOE_HALF_1(s, cur, nxt)                        \
-  issue((s) + 3, r.cur);                               \
+  issue_a((s) + 3, r.cur);                             \
   read_frag(f0, oa, ob, r.nxt, r.nxt + SB, 0);         \
   mfma_frag(acc, f1);                                  \
-  interleave<MI * NB, OpA::READS + OpB::READS, IL>();
-#define MOE_STAGE(s, cur, nxt)                         \
-  MOE_HALF_0(cur)                                      \
+  interleave<MI * NB, OpA::READS + OpB::READS, OpA::IL>();
+#define MOE_STAGE(s, cur, nxt, prv)                    \
+  MOE_HALF_0(s, cur, prv)                              \
   MOE_HALF_1(s, cur, nxt)
-#define MOE_LAST_STAGES(s, cur, nxt)                   \
-  MOE_HALF_0(cur)                                      \
+#define MOE_LAST_STAGES(s, cur, nxt, prv)              \
+  MOE_HALF_0(s, cur, prv)                              \
   if (z && (s) + 2 == stages) zero_terms<OpA, OpB>(r.nxt, r.nxt + SB, z); \
   MOE_HALF_1(s, cur, nxt)
-template <int MI, int NB, class OpA, class OpB, class Issue>
+template <int MI, int NB, class OpA, class OpB, class IssueA, class IssueB>
 __device__ __forceinline__ void run_sum(f32x16 (&acc)[MI][NB], const OpA &oa, const OpB &ob,
-                                        int stages, int z, const Ring3 &r, Issue issue) {
+                                        int stages, int z, const Ring3 &r, IssueA issue_a,
+                                        IssueB issue_b) {
   constexpr int IL = OpA::IL + OpB::IL;
-  issue(0, r.s0);
-  issue(1, r.s1);
-  issue(2, r.s2);
-  wait_vmcnt<2 * IL>();
+  issue_a(0, r.s0);
+  issue_b(0, r.s0 + SB);
+  issue_a(1, r.s1);
+  issue_b(1, r.s1 + SB);
+  issue_a(2, r.s2);
+  wait_vmcnt<IL + OpA::IL>();
   stage_barrier();
   if (z && stages == 1) zero_terms<OpA, OpB>(r.s0, r.s0 + SB, z);
   Frag<MI, NB> f0, f1;
   read_frag(f0, oa, ob, r.s0, r.s0 + SB, 0);
   int s = 0;
   for (; s + 4 < stages; s += 3) {
-    MOE_STAGE(s, s0, s1)
-    MOE_STAGE(s + 1, s1, s2)
-    MOE_STAGE(s + 2, s2, s0)
+    MOE_STAGE(s, s0, s1, s2)
+    MOE_STAGE(s + 1, s1, s2, s0)
+    MOE_STAGE(s + 2, s2, s0, s1)
   }
   if (s < stages) {
-    MOE_LAST_STAGES(s, s0, s1)
+    MOE_LAST_STAGES(s, s0, s1, s2)
     if (s + 1 < stages) {
-      MOE_LAST_STAGES(s + 1, s1, s2)
+      MOE_LAST_STAGES(s + 1, s1, s2, s0)
       if (s + 2 < stages) {
-        MOE_LAST_STAGES(s + 2, s2, s0)
+        MOE_LAST_STAGES(s + 2, s2, s0, s1)
         if (s + 3 < stages) {
-          MOE_LAST_STAGES(s + 3, s0, s1)
+          MOE_LAST_STAGES(s + 3, s0, s1, s2)
         }
       }
     }
@@ -180,15 +184,17 @@ __global__ __launch_bounds__(NW * 64, 2) void wgrad_kernel(const GradArgs a, int
     each_piece<false, 32>(acc, mine, out);
     return;
   }
-  auto issue = [&](int st, u32x4 *slot) {
-    const int t0 = span.first(min(st, span.stages - 1));
-    const uint16_t *const pa = dC + (size_t)t0 * a.N, *const pb = A + (size_t)t0 * a.K;
+  auto issue_a = [&](int st, u32x4 *slot) {
+    const uint16_t *const p = dC + (size_t)span.first(min(st, span.stages - 1)) * a.N;
 #pragma unroll
-    for (int i = 0; i < IA; ++i) load_lds(pa, at_a[i], slot + (wv * IA + i) * 64);
-#pragma unroll
-    for (int i = 0; i < IB; ++i) load_lds(pb, at_b[i], slot + SB + (wv * IB + i) * 64);
+    for (int i = 0; i < IA; ++i) load_lds(p, at_a[i], slot + (wv * IA + i) * 64);
   };
-  run_sum(acc, oa, ob, span.stages, span.back, ring, issue);
+  auto issue_b = [&](int st, u32x4 *slot) {
+    const uint16_t *const p = A + (size_t)span.first(min(st, span.stages - 1)) * a.K;
+#pragma unroll
+    for (int i = 0; i < IB; ++i) load_lds(p, at_b[i], slot + (wv * IB + i) * 64);
+  };
+  run_sum(acc, oa, ob, span.stages, span.back, ring, issue_a, issue_b);
   stage_barrier();  // every wave is done reading the ring
   if (full) each_piece<true, 32>(acc, mine, out);
   else each_piece<false, 32>(acc, mine, out);
