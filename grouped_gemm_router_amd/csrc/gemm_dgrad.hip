@@ -204,7 +204,7 @@ __device__ __forceinline__ float sigmoid(float z) {
 // what becomes of the sums of a dgrad tile
 template <bool SWIGLU, bool OUT_F32, bool STREAM>
 struct DgradOut {
-  static constexpr int COLS = OUT_F32 ? 4 : 8, DEPTH = 2;
+  static constexpr int COLS = OUT_F32 ? 4 : 8, UN = 4, DEPTH = 2;
   const GradArgs &a;
   int m0, mend, k0;
   size_t first;  // where the slice's outputs begin

@@ -175,7 +175,7 @@ __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *m
   constexpr int C = Out::COLS;                 // columns a lane takes: 16 bytes of the output
   constexpr int CH = MI < ROWS / 32 ? MI : ROWS / 32;  // 32-row blocks at a time
   constexpr int ALL = CH * 32 * (W / C) / 64;  // pieces a lane and chunk
-  constexpr int UN = 4, DEPTH = Out::DEPTH;    // pieces a batch, batches asked for ahead
+  constexpr int UN = Out::UN, DEPTH = Out::DEPTH;  // pieces a batch, batches asked for ahead
   constexpr int BATCHES = ALL / UN * (MI / CH);
   static_assert(ALL % UN == 0 && MI % CH == 0, "whole batches");
   const int lane = lane_id(), wv = threadIdx.x / kWave;
@@ -188,8 +188,9 @@ __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *m
       held[b % DEPTH][n] = out.template begin<FULL>(row0 + id / (W / C), col0 + id % (W / C) * C);
     }
   };
+  // (all but two batches once the first blocks have left their registers)
 #pragma unroll
-  for (int b = 0; b < (DEPTH < BATCHES ? DEPTH : BATCHES); ++b) begin(b);
+  for (int b = 0; b < (2 < BATCHES ? 2 : BATCHES); ++b) begin(b);
 #pragma unroll
   for (int b = 0; b < BATCHES; ++b) {
     if (b % (ALL / UN) == 0) {
@@ -205,6 +206,11 @@ __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *m
             const f32x4 v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
             mine[row * PPR + (p ^ (row & 15))] = __builtin_bit_cast(u32x4, v);
           }
+    }
+    if (b == 0) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 2; n < (DEPTH < BATCHES ? DEPTH : BATCHES); ++n) begin(n);
     }
     float v[UN][C];
 #pragma unroll

@@ -82,7 +82,7 @@ enum Mode { PLAIN, STREAM, ADD };  // past the caches; added to what is there
 
 template <bool OUT_F32, Mode MODE>
 struct WgradOut {
-  static constexpr int COLS = OUT_F32 ? 4 : 8, DEPTH = 2;
+  static constexpr int COLS = OUT_F32 ? 4 : 8, UN = 4, DEPTH = 2;
   typedef typename std::conditional<OUT_F32, float, uint16_t>::type T;
   T *out;  // the group's weights
   int N, K, n0, k0;
