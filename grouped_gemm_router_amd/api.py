@@ -765,20 +765,26 @@ def moe_grouped_gemm_wgrad(dC, A, dB, offsets, *, accumulate=False, ws=None, str
 
 _dtype_of = operator.attrgetter("dtype")
 _ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_TENSORS = {torch.Tensor, torch.nn.Parameter}
 
 
 def _grads(grads, name, device):
     """Host arrays (pointers, sizes, types) of a list of gradients."""
-    # (whole lists through map: half the time of a loop over 100 tensors)
+    # (whole lists through map: a third of the time of a loop over 100 tensors)
     T = torch.Tensor
-    if not all(map(isinstance, grads, itertools.repeat(T))):
+    if not set(map(type, grads)) <= _TENSORS and not all(map(isinstance, grads,
+                                                             itertools.repeat(T))):
         raise TypeError("%s must hold torch.Tensors" % name)
     if grads and set(map(T.get_device, grads)) != {device}:
         raise ValueError("%s must be on GPU %d, like norm" % (name, device))
     if not all(map(T.is_contiguous, grads)):
         raise ValueError("%s must be contiguous" % name)
+    types = list(map(_dtype_of, grads))
     try:
-        dts = array.array("i", [_ACT[t] for t in map(_dtype_of, grads)])
+        if len(set(types)) == 1:
+            dts = array.array("i", [_ACT[types[0]]]) * len(types)
+        else:
+            dts = array.array("i", [_ACT[t] for t in types])
     except KeyError as e:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, e.args[0])) from None
     return array.array("Q", map(T.data_ptr, grads)), array.array("q", map(T.numel, grads)), dts

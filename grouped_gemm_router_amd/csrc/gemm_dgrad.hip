@@ -234,7 +234,7 @@ struct DgradOut {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float s = sigmoid(z[i]), zs = z[i] * s;
-        dg[i] = v[i] * u[i] * s * (1.f + z[i] * (1.f - s));
+        dg[i] = v[i] * u[i] * fmaf(zs, 1.f - s, s);  // s (1 + z (1 - s))
         du[i] = v[i] * zs;
         h[i] = zs * u[i];
       }
@@ -263,7 +263,8 @@ __global__ __launch_bounds__(NW * 64, 1) void dgrad_kernel(const GradArgs a, int
   const Tile tile = sc.tile;
   typedef DgradOut<SWIGLU, OUT_F32, STREAM> Out;
   const int rows = tile.mend - tile.m0;
-  if (rows > 128) dgrad_tile<256, SHORT, Out>(a, tile, slice, ring);
+  if (rows > 192) dgrad_tile<256, SHORT, Out>(a, tile, slice, ring);
+  else if (rows > 128) dgrad_tile<192, SHORT, Out>(a, tile, slice, ring);
   else if (rows > 64) dgrad_tile<128, SHORT, Out>(a, tile, slice, ring);
   else dgrad_tile<64, SHORT, Out>(a, tile, slice, ring);
 }

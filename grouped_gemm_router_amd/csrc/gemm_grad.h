@@ -173,7 +173,7 @@ template <bool FULL, int ROWS, int MI, int NB, class Out>
 __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *mine, const Out &out) {
   constexpr int W = NB * 32, PPR = W / 4;      // columns and 16-byte pieces a row
   constexpr int C = Out::COLS;                 // columns a lane takes: 16 bytes of the output
-  constexpr int CH = MI < ROWS / 32 ? MI : ROWS / 32;  // 32-row blocks at a time
+  constexpr int CH = MI % (ROWS / 32) == 0 ? ROWS / 32 : 1;  // 32-row blocks at a time
   constexpr int ALL = CH * 32 * (W / C) / 64;  // pieces a lane and chunk
   constexpr int UN = Out::UN, DEPTH = Out::DEPTH;  // pieces a batch, batches asked for ahead
   constexpr int BATCHES = ALL / UN * (MI / CH);
