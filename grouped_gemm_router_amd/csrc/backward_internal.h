@@ -32,22 +32,16 @@ struct GradArgs {
 
 namespace moe {
 
-// Rows [s[0], s[1]) of group g: group g begins at the largest of
-// clamp(offsets[h], 0, rows) over h <= g, as in the tile scheduler.  The first
-// wave looks at the offsets; s is in LDS.  Must be called by all threads.
+// Rows [*r0, *r1) of group g: group g begins at the largest of
+// clamp(offsets[h], 0, rows) over h <= g, as in the tile scheduler.  Every wave
+// looks for itself (no barrier); must be called by whole waves.
 __device__ __forceinline__ void group_rows(const int32_t *__restrict__ offsets, int rows, int g,
-                                           int *s) {
-  if (threadIdx.x < kWave) {
-    int first = 0;
-    for (int h = threadIdx.x; h <= g; h += kWave) first = max(first, min(offsets[h], rows));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) first = max(first, __shfl_xor(first, o, kWave));
-    if (threadIdx.x == 0) {
-      s[0] = first;
-      s[1] = max(first, min(offsets[g + 1], rows));
-    }
-  }
-  __syncthreads();
+                                           int *r0, int *r1) {
+  int first = 0;
+  for (int h = lane_id(); h <= g; h += kWave) first = max(first, min(offsets[h], rows));
+  const int next = min(offsets[g + 1], rows);
+  *r0 = __builtin_amdgcn_readlane(wave_inclusive_max(first), kWave - 1);
+  *r1 = max(*r0, next);
 }
 
 // The rows of slice i of n: runs of a multiple of 32 rows.

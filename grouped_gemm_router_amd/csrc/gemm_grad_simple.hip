@@ -150,15 +150,14 @@ __global__ __launch_bounds__(256) void dgrad_simple_kernel(const GradArgs a, int
 template <int ES, int OS>
 __global__ __launch_bounds__(256) void wgrad_simple_kernel(const GradArgs a, int nt, int kt) {
   __shared__ Shared s;
-  __shared__ int s_rows[2];
   int w = blockIdx.x;
   const int k0 = w % kt * BT;
   w /= kt;
   const int n0 = w % nt * BT;
   w /= nt;
   const int g = w % a.G, slice = w / a.G;
-  group_rows(a.offsets, a.rows, g, s_rows);
-  int r0 = s_rows[0], r1 = s_rows[1];
+  int r0, r1;
+  group_rows(a.offsets, a.rows, g, &r0, &r1);
   if (a.slices > 1) slice_rows(&r0, &r1, slice, a.slices);
   const int t = threadIdx.x;
   const int ca = n0 + (t % 8) * 8, cb = k0 + (t % 8) * 8;
@@ -213,11 +212,11 @@ __global__ __launch_bounds__(256) void wgrad_reduce_kernel(const GradArgs a) {
 // ES: element size of the operands; rows outside every group are left alone
 template <int ES, int OS, bool SWIGLU>
 __global__ __launch_bounds__(256) void dgrad_reduce_kernel(const GradArgs a) {
-  __shared__ int s_last[2], s_first[2];
-  group_rows(a.offsets, a.rows, a.G - 1, s_last);
-  group_rows(a.offsets, a.rows, 0, s_first);
+  int first, last, r;
+  group_rows(a.offsets, a.rows, 0, &first, &r);
+  group_rows(a.offsets, a.rows, a.G - 1, &r, &last);
   const size_t all = (size_t)a.rows * a.K;
-  const size_t begin = (size_t)s_first[0] * a.K, end = (size_t)s_last[1] * a.K;
+  const size_t begin = (size_t)first * a.K, end = (size_t)last * a.K;
   for (size_t e = begin + ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; e < end;
        e += (size_t)gridDim.x * 256 * 8) {
     float v[8];

@@ -115,7 +115,6 @@ __global__ __launch_bounds__(NW * 64, 2) void wgrad_kernel(const GradArgs a, int
   constexpr int IA = OpA::IL, IB = OpB::IL;
   __shared__ u32x4 s0[SLOT], s1[SLOT], s2[2048];  // 80 KB
   const Ring3 ring = {s0, s1, s2};
-  int *const s_rows = reinterpret_cast<int *>(s2);  // until the ring starts
   const int all = nt * kt * a.G * a.slices;
   int w = blockIdx.x;
   if (w < all / 512 * 512) w = w / 512 * 512 + (w % 8) * 64 + w % 512 / 8;
@@ -127,9 +126,8 @@ __global__ __launch_bounds__(NW * 64, 2) void wgrad_kernel(const GradArgs a, int
   const int k0 = in / wide * 256;
   const int n0 = (strip * kStrip + in % wide) * 128;
   const int g = w % a.G, slice = w / a.G;
-  group_rows(a.offsets, a.rows, g, s_rows);
-  int r0 = s_rows[0], r1 = s_rows[1];
-  __syncthreads();
+  int r0, r1;
+  group_rows(a.offsets, a.rows, g, &r0, &r1);
   if (a.slices > 1) slice_rows(&r0, &r1, slice, a.slices);
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   // bytes from the stage's first row in the tile's first column; columns past
