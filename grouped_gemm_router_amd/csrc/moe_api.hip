@@ -493,6 +493,8 @@ moe_status_t grad_sizes(int G, int rows, int N, int K, int *ldb, moe_dtype_t dt)
   if (!is_act(dt) || G > MOE_MAX_GROUPS || N % 8 != 0 || K % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (*ldb == 0) *ldb = K;
   if (*ldb < K || (long long)*ldb * size_of(dt) % 16 != 0) return MOE_ERR_INVALID;
+  // (offsets inside a tile, up to 256 rows, are 32-bit)
+  if (N >= MOE_MAX_GRAD_WIDTH || *ldb >= MOE_MAX_GRAD_WIDTH) return MOE_ERR_UNSUPPORTED;
   if ((long long)G * N * *ldb >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
   // (a launch has fewer than 2^32 threads, 256 for each 64 x 64 outputs)
   const long long tn = (N + 63) / 64, tk = (K + 63) / 64;
@@ -551,8 +553,8 @@ moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void 
   const moe_status_t sizes = sort_sizes(T, k, d, n_shared);
   if (sizes != MOE_OK) return sizes;
   if (!is_act(dt) || !is_act(y_dt)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;  // (of pointers nothing is asked: empty arrays have none)
   if (!dY && !d_topk_w) return MOE_ERR_INVALID;
-  if (T == 0) return MOE_OK;
   if (!aligned16(d_out) || !aligned4(flat_to_row) || !aligned4(topk_w) || !opt_aligned16(dY) ||
       !opt_aligned4(d_topk_w) || (d_topk_w ? !aligned16(Y) : Y != nullptr))
     return MOE_ERR_INVALID;
@@ -589,8 +591,8 @@ moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *d
   const moe_status_t sizes = grad_sizes(G, rows, N, K, &ldb, dt);
   if (sizes != MOE_OK) return sizes;
   if (a_dt != dt && a_dt != MOE_F32) return MOE_ERR_UNSUPPORTED;
-  if ((dC2 == nullptr) != (B2 == nullptr)) return MOE_ERR_INVALID;
   if (rows == 0) return MOE_OK;
+  if ((dC2 == nullptr) != (B2 == nullptr)) return MOE_ERR_INVALID;
   if (!aligned16(dC) || !aligned16(B) || !opt_aligned16(dC2) || !opt_aligned16(B2) ||
       !aligned16(dA) || !aligned4(offsets))
     return MOE_ERR_INVALID;

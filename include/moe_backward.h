@@ -83,8 +83,13 @@ moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
  * or MOE_F32.  dA may not be dC or dC2.  ws (device, 16-byte aligned) must
  * hold moe_grouped_gemm_dgrad_workspace_size bytes (else MOE_ERR_WORKSPACE;
  * NULL with ws_bytes 0 where that is 0); calls that share it must be ordered.
- * Requires N % 8 == 0, K % 8 == 0, 1 <= G <= MOE_MAX_GROUPS.
+ * Few tiles with long sums are cut along N; the slices' fp32 sums lie in ws and
+ * are added in a fixed order.
+ * Requires N % 8 == 0, K % 8 == 0, N and ldb < MOE_MAX_GRAD_WIDTH,
+ * 1 <= G <= MOE_MAX_GROUPS, and fewer than 2^24 tiles of 64 x 64 outputs
+ * ((rows / 64 + G) K / 64; for the weights G N K / 4096).
  */
+#define MOE_MAX_GRAD_WIDTH (1 << 23)
 moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *dC2,
                                     const void *B2, moe_dtype_t dt, void *dA, moe_dtype_t a_dt,
                                     const int32_t *offsets, int G, int rows, int N, int K,
@@ -117,8 +122,8 @@ size_t moe_grouped_gemm_dgrad_workspace_size(int G, int rows, int N, int K, moe_
  * are not used and may hold anything.  dC [rows][N], A [rows][K] of type dt,
  * dB [G][N][K] dense, of type b_dt: dt or MOE_F32.  With accumulate != 0 the
  * sum is added in fp32 to what dB holds and rounded once.  ws as for
- * moe_grouped_gemm_dgrad, of moe_grouped_gemm_wgrad_workspace_size bytes.
- * Requires N % 8 == 0, K % 8 == 0, 1 <= G <= MOE_MAX_GROUPS.
+ * moe_grouped_gemm_dgrad (the sums are cut along a group's rows), of
+ * moe_grouped_gemm_wgrad_workspace_size bytes.  Sizes as there.
  */
 moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t dt, void *dB,
                                     moe_dtype_t b_dt, const int32_t *offsets, int G, int rows,

@@ -68,8 +68,15 @@ def test_dgrad_validation(lib):
         assert f(**bad) == INVALID, bad
     for bad in (dict(G=1041), dict(N=60), dict(K=60), dict(dt=E4M3), dict(adt=E4M3),
                 dict(dt=F32, adt=BF16), dict(N=1 << 24, K=1 << 20),
-                dict(rows=1 << 30, K=1 << 16)):
+                dict(rows=1 << 30, K=1 << 16), dict(N=1 << 23, K=8), dict(K=8, ldb=1 << 23)):
         assert f(**bad) == UNSUPPORTED, bad
+    size = lib.moe_grouped_gemm_dgrad_workspace_size  # few tiles, long sums: slices
+    need = size(2, 16, 4096, 64, BF16)
+    assert need >= 2 * 16 * 64 * 4 and size(2, 16, 4096, 64, F32) > 0
+    assert size(8, 8192, 4096, 14336, BF16) == 0 == size(0, 16, 4096, 64, BF16)
+    assert size(2, 16, 4096, 60, BF16) == 0
+    assert f(N=4096, ws=P5, wsb=need - 1) == WORKSPACE and f(N=4096) == WORKSPACE
+    assert f(N=4096, ws=MIS, wsb=need) == INVALID
 
 
 def test_dgrad_swiglu_validation(lib):
@@ -97,8 +104,12 @@ def test_wgrad_validation(lib):
                 dict(dB=NUL), dict(dB=P), dict(dB=P2), dict(off=NUL)):
         assert f(**bad) == INVALID, bad
     for bad in (dict(G=2000), dict(N=60), dict(K=60), dict(dt=E4M3), dict(bdt=E4M3),
-                dict(dt=F32, bdt=BF16), dict(N=1 << 20, K=1 << 20)):
+                dict(dt=F32, bdt=BF16), dict(N=1 << 20, K=1 << 20), dict(N=1 << 23, K=8)):
         assert f(**bad) == UNSUPPORTED, bad
+    need = lib.moe_grouped_gemm_wgrad_workspace_size(1, 4096, 64, 64, BF16)
+    assert need >= 2 * 64 * 64 * 4
+    assert f(G=1, rows=4096, ws=P5, wsb=need - 1) == WORKSPACE
+    assert lib.moe_grouped_gemm_wgrad_workspace_size(8, 8192, 14336, 4096, BF16) == 0
     assert lib.moe_grouped_gemm_wgrad_workspace_size(0, 1, 8, 8, BF16) == 0
     assert lib.moe_grouped_gemm_wgrad_workspace_size(1, 1, 9, 8, BF16) == 0
 

@@ -148,3 +148,48 @@ def test_a_captured_backward_pass():
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(got[n], want[n]) and torch.equal(eager[n], want[n]), n
+
+
+def test_another_batch_size():
+    """A forward of other tokens replaces what backward works on."""
+    m, w, x, d_out = build(40, 64, 128, 4, 2, 1, BF)
+    m(x)
+    first = {n: t.clone() for n, t in m.backward(d_out).items()}
+    m(x[:7].contiguous())
+    small = m.backward(d_out[:7].contiguous())
+    assert small["dx"].shape == (7, 64)
+    with pytest.raises(ValueError, match="d_out"):
+        m.backward(d_out)
+    m(x)
+    again = m.backward(d_out)
+    assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def test_no_tokens():
+    """The operators of a step take a batch of no tokens (the layer's forward
+    pass refuses one)."""
+    from grouped_gemm_router_amd import api
+    e = lambda *s, dt=BF: torch.empty(s, dtype=dt, device=DEV)  # noqa: E731
+    i32 = torch.int32
+    api.moe_combine_backward(e(0, 64), e(0, 64, dt=F32), e(0, dt=i32), e(0, 2, dt=F32), e(0, 64),
+                             e(0, 2, dt=F32), n_shared=1)
+    api.moe_permute_backward(e(0, 64), e(0, dt=i32), e(0, 64), 2, addend=e(0, 64))
+    off = torch.zeros((4,), dtype=i32, device=DEV)
+    W, dW = e(3, 128, 64), torch.full((3, 128, 64), 7.0, dtype=BF, device=DEV)
+    api.moe_grouped_gemm_dgrad(e(0, 128), W, e(0, 64), off, dC2=e(0, 128), B2=W)
+    api.moe_grouped_gemm_dgrad_swiglu(e(0, 128), W, *(e(0, 64) for _ in range(4)), off)
+    api.moe_grouped_gemm_wgrad(e(0, 128), e(0, 64), dW, off)
+    assert (dW == 0).all()
+
+
+def test_on_another_stream():
+    m, w, x, d_out = build(64, 128, 256, 8, 2, 1, BF)
+    m(x)
+    want = m.backward(d_out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m(x)
+        got = m.backward(d_out)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(got[n], want[n]) for n in want)
