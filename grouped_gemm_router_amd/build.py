@@ -22,7 +22,7 @@ SOURCES = ["moe_api.hip", "route.hip", "permute.hip", "gemm_bf16.hip", "gemm_fp8
            "gemm_simple.hip", "combine.hip", "quant.hip", "router_stats.hip", "balance.hip",
            "lora_plan.hip", "lora_shrink.hip", "lora_expand.hip", "lora_wgrad.hip",
            "sort_backward.hip", "gemm_dgrad.hip", "gemm_wgrad.hip",
-           "gemm_grad_simple.hip", "grad_norm.hip"]
+           "gemm_grad_f32.hip", "gemm_grad_slices.hip", "grad_norm.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

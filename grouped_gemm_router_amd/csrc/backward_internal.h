@@ -54,14 +54,25 @@ __device__ __forceinline__ void slice_rows(int *r0, int *r1, int i, int n) {
 
 }  // namespace moe
 
-hipError_t launch_dgrad_simple(const GradArgs &a, hipStream_t s);
-hipError_t launch_wgrad_simple(const GradArgs &a, hipStream_t s);
+hipError_t launch_dgrad_f32(const GradArgs &a, hipStream_t s);
+hipError_t launch_wgrad_f32(const GradArgs &a, hipStream_t s);
 hipError_t launch_dgrad_bf16(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_bf16(const GradArgs &a, hipStream_t s);
 // the slices' sums added in slice order and stored as the launch without slices
 // would (dgrad: the rows of all groups)
 hipError_t launch_dgrad_reduce(const GradArgs &a, hipStream_t s);
 hipError_t launch_wgrad_reduce(const GradArgs &a, hipStream_t s);
+
+// The arguments of a launch that writes slices: plain fp32 sums.
+inline GradArgs to_slices(GradArgs a) {
+  if (a.slices > 1) {
+    a.out = a.part;
+    a.out_dt = MOE_F32;
+    a.gate = nullptr;
+    a.accumulate = 0;
+  }
+  return a;
+}
 
 // Row tiles of BM rows that groups can have: at most one partly filled tile for
 // each group with a row.

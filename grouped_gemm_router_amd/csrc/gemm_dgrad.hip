@@ -1,6 +1,30 @@
 // gemm_dgrad.hip -- the gradient of a grouped product's input on bf16 MFMA:
 //   dA[r][k] = sum_n dC[r][n] B[g][n][k] (+ dC2 B2), r in group g,
 // with SwiGLU's gradient behind it or not.
+//
+// Design (what is shared with gemm_wgrad.hip stands in gemm_grad.h):
+//   * tiles of 256 x 256 outputs, one workgroup of 4 waves (128 x 128 each) a
+//     CU, and tiles of 192, 128 or 64 rows for what a group leaves; the device
+//     reads the offsets (the tile scheduler of the forward product);
+//   * stages of 64 terms: dC, whose rows lie along the sum, moves as whole
+//     128-byte lines (as 64-byte halves, twice the requests: 8 groups of 1024,
+//     N 4096, K 14336 took 842 us instead of 779), the weights as they lie;
+//   * half a stage's LDS reads go between the first MFMAs of the half before
+//     (left to the compiler, each half waited for its own reads: 887 -> 847);
+//   * a sum that ends inside a stage moves its last stage back instead of
+//     testing every load (that arithmetic, 10 instructions a load, no longer
+//     fitted beside the MFMAs); the second of two products follows in the same
+//     run of stages.
+// Measured on that shape: 750-820 us a box, 1.17-1.28 PFLOP/s (the library's
+// dense product of the same sizes 1.31, its 8192^3 with both operands along the
+// sum 1.51).  The matrix cores are busy 69 % of the cycles, at 1.69 GHz: the
+// chip lowers its clock under this load, so that fewer stalls buy less than
+// their share.  SwiGLU's gradient adds 230 us there: 1.17 GB read and written
+// (230 us at 5.05 TB/s) by waves that do nothing else meanwhile.  Measured and
+// not kept for it: eight waves of 128 x 64 (no faster, the product 3 % slower),
+// two workgroups a CU of 256 x 128 tiles (1136 against 989 us at the time),
+// loads asked for further ahead (no change, then spills), workgroups started
+// apart (1078 -> 1068 at best), 32 instead of 16 columns of tiles in turn.
 #include "gemm_grad.h"
 
 namespace {
@@ -277,12 +301,7 @@ __global__ __launch_bounds__(NW * 64, 1) void dgrad_kernel(const GradArgs a, int
 }  // namespace
 
 hipError_t launch_dgrad_bf16(const GradArgs &args, hipStream_t s) {
-  GradArgs a = args;
-  if (a.slices > 1) {
-    a.out = a.part;
-    a.out_dt = MOE_F32;
-    a.gate = nullptr;
-  }
+  const GradArgs a = to_slices(args);
   const int nt = (a.K + 255) / 256;
   const dim3 grid((unsigned)(row_tiles(a.rows, a.G, 256) * (long long)nt * a.slices)), block(NW * 64);
   const bool brief = a.N < 64;

@@ -262,8 +262,9 @@ __device__ __forceinline__ void store(float *p, const float *v) {
 }
 
 // Outputs that the 256 MB last-level cache cannot keep for their reader go past
-// it, where rows are whole 128-byte lines (a line that two stores fill costs
-// more that way).
+// it, where rows are whole 128-byte lines (64 groups' weights of 1408 x 2048 in
+// bf16 271 -> 210 us, 14336 x 4096 1013 -> 980; a line that two stores fill
+// costs more that way: 1416 x 2056 in fp32 434 -> 474).
 inline bool streams(size_t rows, int row_bytes, int arrays) {
   return row_bytes % 128 == 0 && rows * row_bytes * arrays > (256u << 20);
 }

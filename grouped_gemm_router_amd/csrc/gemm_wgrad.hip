@@ -1,5 +1,19 @@
 // gemm_wgrad.hip -- the gradient of a grouped product's weights on bf16 MFMA:
 //   dB[g][n][k] (+)= sum_{r in group g} dC[r][n] A[r][k]
+//
+// Design (what is shared with gemm_dgrad.hip stands in gemm_grad.h): sums are
+// as long as a group has rows (1024 on the Mixtral shapes, some hundreds for
+// fine-grained experts), so what a tile does besides its sum counts: tiles of
+// 128 x 256 weights, 4 waves of 64 x 128, two workgroups a CU, so that one's
+// sum runs beside the other's start and stores (256 x 256 tiles, one a CU: 8
+// groups of 1024 rows, 14336 x 4096: 999 against 946 us in one process; 64
+// groups of 384, 1408 x 2048: 250 against 193).  Both operands' rows are terms;
+// stages of 32 rows of whole 256- and 512-byte pieces.
+// Measured: 14336 x 4096 in bf16, 8192 rows of 8 groups 935-1000 us (1.0
+// PFLOP/s; the library's single product of a group 0.84): matrix cores 58 %
+// busy at 1.68 GHz, 0.94 GB of weights written (186 us at 5.05 TB/s) partly
+// beside the sums.  1416 x 2056 in fp32, 24271 rows of 64 groups 361-395 us:
+// 150 of sums, the rest 745 MB of rows that begin inside a 128-byte line.
 #include <type_traits>
 
 #include "gemm_grad.h"
@@ -75,7 +89,11 @@ __device__ __forceinline__ void run_sum(f32x16 (&acc)[MI][NB], const OpA &oa, co
 #undef MOE_HALF_1
 #undef MOE_HALF_0
 
-constexpr int kStrip = 6;
+// Tiles run in strips of kStrip tiles of n, along k, and an XCD takes 64
+// consecutive ones (what its 32 CUs hold), so that its L2 is asked for few
+// columns of either operand (columns of k in turn over all XCDs: 1013 -> 986 us
+// on 8 groups of 14336 x 4096; strips of 4, 8 or 12, or along n: within 3 %).
+constexpr int kStrip = 6, kRun = 64;
 
 // how the sums of a wgrad tile are stored
 enum Mode { PLAIN, STREAM, ADD };  // past the caches; added to what is there
@@ -117,7 +135,8 @@ __global__ __launch_bounds__(NW * 64, 2) void wgrad_kernel(const GradArgs a, int
   const Ring3 ring = {s0, s1, s2};
   const int all = nt * kt * a.G * a.slices;
   int w = blockIdx.x;
-  if (w < all / 512 * 512) w = w / 512 * 512 + (w % 8) * 64 + w % 512 / 8;
+  if (w < all / (8 * kRun) * (8 * kRun))
+    w = w / (8 * kRun) * (8 * kRun) + w % 8 * kRun + w / 8 % kRun;
   const int per = nt * kt;
   const int t = w % per;
   w /= per;
@@ -201,14 +220,9 @@ __global__ __launch_bounds__(NW * 64, 2) void wgrad_kernel(const GradArgs a, int
 }  // namespace
 
 hipError_t launch_wgrad_bf16(const GradArgs &args, hipStream_t s) {
-  GradArgs a = args;
+  const GradArgs a = to_slices(args);
   const int nt = (a.N + 127) / 128, kt = (a.K + 255) / 256;
   const dim3 grid((unsigned)((long long)a.slices * a.G * nt * kt)), block(NW * 64);
-  if (a.slices > 1) {
-    a.out = a.part;
-    a.out_dt = MOE_F32;
-    a.accumulate = 0;
-  }
   const bool f32 = a.out_dt == MOE_F32;
   const Mode mode = a.accumulate ? ADD
                     : a.slices == 1 && streams((size_t)a.G * a.N, a.K * (f32 ? 4 : 2), 1) ? STREAM

@@ -516,12 +516,12 @@ int grad_cus() {
 }
 
 hipError_t launch_dgrad(const GradArgs &a, hipStream_t s) {
-  const hipError_t e = a.dt == MOE_BF16 ? launch_dgrad_bf16(a, s) : launch_dgrad_simple(a, s);
+  const hipError_t e = a.dt == MOE_BF16 ? launch_dgrad_bf16(a, s) : launch_dgrad_f32(a, s);
   return e == hipSuccess && a.slices > 1 ? launch_dgrad_reduce(a, s) : e;
 }
 
 hipError_t launch_wgrad(const GradArgs &a, hipStream_t s) {
-  const hipError_t e = a.dt == MOE_BF16 ? launch_wgrad_bf16(a, s) : launch_wgrad_simple(a, s);
+  const hipError_t e = a.dt == MOE_BF16 ? launch_wgrad_bf16(a, s) : launch_wgrad_f32(a, s);
   return e == hipSuccess && a.slices > 1 ? launch_wgrad_reduce(a, s) : e;
 }
 
