@@ -4,8 +4,9 @@
           -> combine
 
 ("Dense GEMM to TP MoE" §2.2 data flow; "DeepGEMM walkthrough" §2.1 layer
-formula with the shared expert.)  This module only allocates buffers with
-torch and passes pointers; every step runs in the library's HIP kernels, on
+formula with the shared expert.)  ``backward`` runs the calls of
+``include/moe_backward.h`` behind a forward pass.  This module only allocates
+buffers with torch and passes pointers; every step runs in the library's HIP kernels, on
 the current stream, with no host synchronisation and no host round trip of
 the per-expert sizes.
 """
