@@ -150,18 +150,22 @@ def _check(fn: str, status: int) -> None:
         raise MoEError(fn, status)
 
 
-_defer = threading.local()
+class _Defer(threading.local):
+    on = False
+
+
+_defer = _Defer()
 
 
 def _deferring() -> bool:
-    return getattr(_defer, "on", False)
+    return _defer.on
 
 
 def _invoke(fn: str, cfn, *args, keep=None):
     """Call the library entry cfn with marshalled args and check the status;
     inside deferred(), return that call as a thunk instead of making it, which
     holds `keep`, host memory that args point to."""
-    if _deferring():
+    if _defer.on:
         def call(keep=keep):
             status = cfn(*args)
             if status != MOE_OK:
@@ -652,12 +656,14 @@ def moe_permute_backward(dx_perm, flat_to_row, dx, k, *, n_shared=0, addend=None
                    _arg(dx, "dx", dx.dtype, (T, d), dev), _act(dx, "dx"), _raw_stream(stream, dev))
 
 
+_ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _act(t, name) -> int:
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    dt = _ACT.get(t.dtype)
+    if dt is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return dt
 
 
 def _experts(B, name, dtype, N, device):
@@ -764,7 +770,6 @@ def moe_grouped_gemm_wgrad(dC, A, dB, offsets, *, accumulate=False, ws=None, str
 
 
 _dtype_of = operator.attrgetter("dtype")
-_ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _TENSORS = {torch.Tensor, torch.nn.Parameter}
 
 
@@ -790,6 +795,11 @@ def _grads(grads, name, device):
     return array.array("Q", map(T.data_ptr, grads)), array.array("q", map(T.numel, grads)), dts
 
 
+def _listed(tensors):
+    """A list or tuple as it is, anything else (a generator) as a list."""
+    return tensors if isinstance(tensors, (list, tuple)) else list(tensors)
+
+
 def _at(a):
     """Address of an array's first element."""
     return a.buffer_info()[0]
@@ -805,6 +815,7 @@ def moe_grad_norm(grads, norm, *, ws=None, stream=None):
     moe_grad_norm_workspace_size(len(grads)) bytes; when None, one is allocated
     here for this call."""
     dev = _gpu(norm, "norm")
+    grads = _listed(grads)
     host = ptrs, sizes, dts = _grads(grads, "grads", dev)
     pw, wb, ws = _own_workspace(ws, dev, stream, moe_grad_norm_workspace_size, len(grads))
     return _invoke("moe_grad_norm", lib.moe_grad_norm, _at(ptrs), _at(sizes), _at(dts), len(grads),
@@ -817,10 +828,11 @@ def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
     on the device: in place, or into the tensors of out (of the gradients'
     sizes and types; one may be its gradient)."""
     dev = _gpu(norm, "norm")
+    grads = _listed(grads)
     ptrs, sizes, dts = _grads(grads, "grads", dev)
     outs = None
     if out is not None:
-        outs, osizes, odts = _grads(out, "out", dev)
+        outs, osizes, odts = _grads(_listed(out), "out", dev)
         if osizes != sizes or odts != dts:
             raise ValueError("out must have the gradients' sizes and types")
     return _invoke("moe_grad_clip", lib.moe_grad_clip, _at(ptrs), _at(sizes), _at(dts), len(grads),

@@ -15,7 +15,7 @@
 //     testing every load (that arithmetic, 10 instructions a load, no longer
 //     fitted beside the MFMAs); the second of two products follows in the same
 //     run of stages.
-// Measured on that shape: 750-820 us a box, 1.17-1.28 PFLOP/s (the library's
+// Measured on that shape: 750-820 us, from card to card, 1.17-1.28 PFLOP/s (the library's
 // dense product of the same sizes 1.31, its 8192^3 with both operands along the
 // sum 1.51).  The matrix cores are busy 69 % of the cycles, at 1.69 GHz: the
 // chip lowers its clock under this load, so that fewer stalls buy less than

@@ -158,9 +158,10 @@ size_t moe_grad_norm_workspace_size(int n);
  *   out[i][e] = grads[i][e] * min(1, max_norm / (*norm + 1e-6))
  * in fp32, rounded once; out[i] of grads[i]'s size and type.  out == NULL
  * scales in place; out[i] may also be grads[i], but no output may overlap
- * another gradient in part.  Where the factor is 1, what is in place is left
- * alone (bit for bit) and the rest copied.  A norm of NaN makes every value
- * NaN, an infinite norm every finite one 0.  Arrays as in moe_grad_norm.
+ * another gradient or output, nor its own gradient in part.  Where the factor
+ * is 1, what is in place is left alone (bit for bit) and the rest copied.  A
+ * norm of NaN makes every value NaN, an infinite norm every finite one 0.
+ * Arrays as in moe_grad_norm.
  * Requires max_norm >= 0 and finite.
  */
 moe_status_t moe_grad_clip(const void *const *grads, const int64_t *sizes,

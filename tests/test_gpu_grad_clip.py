@@ -205,3 +205,12 @@ def test_a_deferred_step():
         want = norm64(grads)
         close(norm, want, 1)
         assert norm64(out) == pytest.approx(0.5, rel=0.01)
+
+
+def test_any_iterable_of_gradients():
+    grads, _ = make([500, 70], [F32, BF], 1)
+    want = norm64(grads)
+    n = norm_of(g for g in grads)
+    close(n, want, 600)
+    api().moe_grad_clip((g for g in grads), n, want / 2)
+    assert norm64(grads) == pytest.approx(want / 2, rel=0.01)
