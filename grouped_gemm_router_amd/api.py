@@ -826,7 +826,8 @@ def moe_grad_norm(grads, norm, *, ws=None, stream=None):
 def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
     """Scale every gradient by min(1, max_norm / (norm + 1e-6)), norm [1] fp32
     on the device: in place, or into the tensors of out (of the gradients'
-    sizes and types; one may be its gradient)."""
+    sizes and types; one may be its gradient).  Nothing written may overlap
+    the norm or another gradient or output: a shared tensor is given once."""
     dev = _gpu(norm, "norm")
     grads = _listed(grads)
     ptrs, sizes, dts = _grads(grads, "grads", dev)

@@ -1,12 +1,16 @@
 // moe_api.hip -- the extern "C" entry points of libmoe.so (declared and
 // documented in include/moe.h, moe_balance.h, moe_lora.h and
-// moe_backward.h).  Each entry point checks its arguments on the host, returns a status without launching
-// anything if they are bad, and otherwise enqueues the kernels on the
-// caller's stream.  Nothing here allocates, frees, synchronises or reads
-// device memory.
+// moe_backward.h).  Each entry point checks its arguments on the host, returns
+// a status without launching anything if they are bad, and otherwise enqueues
+// the kernels on the caller's stream.  Nothing here allocates, frees,
+// synchronises or reads device memory; host memory is only taken for the
+// length of a clip of many gradients, to sort their ranges.
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
+#include <memory>
+#include <new>
 
 #include "backward_internal.h"
 #include "balance_internal.h"
@@ -544,6 +548,46 @@ moe_status_t grad_list(const void *const *grads, const int64_t *sizes, const moe
   return MOE_OK;
 }
 
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+
+// MOE_OK if nothing that a clip writes is also written by another gradient or
+// read for one (the same tensor twice would be scaled once or twice, as its
+// workgroups happen to run).  An output that is its own gradient is one range.
+moe_status_t clip_ranges(const void *const *grads, const int64_t *sizes, const moe_dtype_t *dts,
+                         int n, const float *norm, void *const *out) {
+  Range few[256];
+  std::unique_ptr<Range[]> many;
+  Range *r = few;
+  if (2 * n + 1 > 256) {
+    many.reset(new (std::nothrow) Range[2 * n + 1]);
+    if (!many) return MOE_ERR_LAUNCH;
+    r = many.get();
+  }
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * size_of(dts[i]);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+    const uintptr_t o = out ? reinterpret_cast<uintptr_t>(out[i]) : g;
+    r[m++] = {o, o + bytes, true};
+    if (o != g) r[m++] = {g, g + bytes, false};
+  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+  r[m++] = {at, at + sizeof(float), false};
+  const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
+  if (!std::is_sorted(r, r + m, before)) std::sort(r, r + m, before);
+  uintptr_t any = 0, written = 0;  // ends of the ranges passed
+  for (int i = 0; i < m; ++i) {
+    if (r[i].begin < (r[i].written ? any : written)) return MOE_ERR_INVALID;
+    any = std::max(any, r[i].end);
+    if (r[i].written) written = std::max(written, r[i].end);
+  }
+  return MOE_OK;
+}
+
 }  // namespace
 
 moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void *Y,
@@ -686,6 +730,8 @@ moe_status_t moe_grad_clip(const void *const *grads, const int64_t *sizes, const
   for (int i = 0; out && i < n; ++i)
     if (sizes[i] > 0 && (!out[i] || reinterpret_cast<uintptr_t>(out[i]) % size_of(dts[i]) != 0))
       return MOE_ERR_INVALID;
+  const moe_status_t apart = clip_ranges(grads, sizes, dts, n, norm, out);
+  if (apart != MOE_OK) return apart;
   return launched(launch_grad_clip(grads, sizes, reinterpret_cast<const int *>(dts), n, norm,
                                    max_norm, out, as_stream(stream)));
 }

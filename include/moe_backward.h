@@ -157,10 +157,10 @@ size_t moe_grad_norm_workspace_size(int n);
  * summed over several GPUs):
  *   out[i][e] = grads[i][e] * min(1, max_norm / (*norm + 1e-6))
  * in fp32, rounded once; out[i] of grads[i]'s size and type.  out == NULL
- * scales in place; out[i] may also be grads[i], but no output may overlap
- * another gradient or output, nor its own gradient in part.  Where the factor
- * is 1, what is in place is left alone (bit for bit) and the rest copied.  A
- * norm of NaN makes every value NaN, an infinite norm every finite one 0.
+ * scales in place; out[i] may also be grads[i].  MOE_ERR_INVALID where an
+ * output overlaps the norm, another gradient or output (the same tensor twice)
+ * or its own gradient in part.  Where the factor is 1, what is in place is left
+ * alone (bit for bit) and the rest copied.  A norm of NaN makes every value NaN, an infinite norm every finite one 0.
  * Arrays as in moe_grad_norm.
  * Requires max_norm >= 0 and finite.
  */

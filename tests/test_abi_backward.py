@@ -149,6 +149,30 @@ def test_grad_norm_and_clip_validation(lib):
     assert clip() == OK and clip((0, 0, F32)) == OK  # nothing to scale
 
 
+@pytest.mark.parametrize("n", [0, 300])  # the ranges of few and of many tensors
+def test_grad_clip_refuses_outputs_that_overlap(lib, n):
+    """Refused before anything is launched: each call here overlaps once."""
+    rest = [(0x100000 + 64 * ((i * 7) % 300), 16, F32) for i in range(n)]
+    norm = 0x9000
+
+    def clip(t, out=None, nrm=norm):
+        t = rest + t
+        o = None if out is None else (C.c_void_p * len(t))(*([r[0] for r in rest] + out))
+        return lib.moe_grad_clip(*lists(*t), C.c_void_p(nrm), 1.0, o, NUL)
+
+    a, b = (0x10000, 8, F32), (0x20000, 8, F32)
+    assert clip([a, b, a]) == INVALID                       # the same one twice
+    assert clip([a, (0x1001C, 8, F32)]) == INVALID          # its last value
+    assert clip([(0x1001C, 8, F32), a]) == INVALID
+    assert clip([(0x10000, 64, F32), (0x10010, 2, BF16), b]) == INVALID  # one inside another
+    assert clip([a, b], nrm=0x1001C) == INVALID             # the norm
+    assert clip([a, b], [0x30000, 0x30010]) == INVALID      # two outputs
+    assert clip([a, b], [0x10004, 0x20000]) == INVALID      # its own gradient in part
+    assert clip([a, b], [0x20000, 0x10000]) == INVALID      # each other's gradient
+    assert clip([a, b], [0x30000, 0x10010]) == INVALID
+    assert clip([a, a], [0x30000, 0x10000]) == INVALID      # read for one, written by the other
+
+
 def test_binding_refuses_host_tensors():
     """No call reaches the library with memory that a GPU cannot read."""
     from grouped_gemm_router_amd import api

@@ -214,3 +214,25 @@ def test_any_iterable_of_gradients():
     close(n, want, 600)
     api().moe_grad_clip((g for g in grads), n, want / 2)
     assert norm64(grads) == pytest.approx(want / 2, rel=0.01)
+
+
+@pytest.mark.parametrize("n", [1, 200])  # the ranges of few and of many tensors
+def test_neighbours_and_shared_sources_are_no_overlap(n):
+    """Outputs that touch, in any order, and one gradient read for several."""
+    store = torch.randn((n * 70 + 1,), device=DEV)
+    parts = [store[70 * i:70 * i + 70] for i in range(n)][::-1]
+    norm = torch.full((1,), 4.0, device=DEV)
+    scale = 2.0 / (torch.tensor(4.0) + 1e-6)
+    want = [p * scale.to(DEV) for p in parts]
+    empty = store[3:3]
+    out = [torch.empty_like(p) for p in parts]
+    first = torch.empty_like(parts[0])
+    api().moe_grad_clip(parts + [parts[0], empty, empty], norm, 2.0, out=out + [first, empty, empty])
+    api().moe_grad_clip(parts + [empty, empty], norm, 2.0)
+    for w, o, p in zip(want, out, parts):
+        assert torch.allclose(o, w, rtol=4 * U, atol=0) and torch.equal(o, p)
+    assert torch.equal(first, out[0])
+    with pytest.raises(api().MoEError):
+        api().moe_grad_clip(parts + parts[:1], norm, 2.0)
+    for w, p in zip(out, parts):
+        assert torch.equal(w, p)
