@@ -164,7 +164,8 @@ def _deferring() -> bool:
 def _invoke(fn: str, cfn, *args, keep=None):
     """Call the library entry cfn with marshalled args and check the status;
     inside deferred(), return that call as a thunk instead of making it, which
-    holds `keep`, host memory that args point to."""
+    holds `keep`: host memory that args point to, and tensors that came in a
+    list (the caller may empty it, or have given a generator)."""
     if _defer.on:
         def call(keep=keep):
             status = cfn(*args)
@@ -796,8 +797,8 @@ def _grads(grads, name, device):
 
 
 def _listed(tensors):
-    """A list or tuple as it is, anything else (a generator) as a list."""
-    return tensors if isinstance(tensors, (list, tuple)) else list(tensors)
+    """The tensors of any iterable, held whatever becomes of it."""
+    return tuple(tensors)
 
 
 def _at(a):
@@ -820,7 +821,7 @@ def moe_grad_norm(grads, norm, *, ws=None, stream=None):
     pw, wb, ws = _own_workspace(ws, dev, stream, moe_grad_norm_workspace_size, len(grads))
     return _invoke("moe_grad_norm", lib.moe_grad_norm, _at(ptrs), _at(sizes), _at(dts), len(grads),
                    _arg(norm, "norm", torch.float32, (1,), dev), pw, wb, _raw_stream(stream, dev),
-                   keep=host)
+                   keep=(host, grads))
 
 
 def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
@@ -833,10 +834,11 @@ def moe_grad_clip(grads, norm, max_norm, *, out=None, stream=None):
     ptrs, sizes, dts = _grads(grads, "grads", dev)
     outs = None
     if out is not None:
-        outs, osizes, odts = _grads(_listed(out), "out", dev)
+        out = _listed(out)
+        outs, osizes, odts = _grads(out, "out", dev)
         if osizes != sizes or odts != dts:
             raise ValueError("out must have the gradients' sizes and types")
     return _invoke("moe_grad_clip", lib.moe_grad_clip, _at(ptrs), _at(sizes), _at(dts), len(grads),
                    _arg(norm, "norm", torch.float32, (1,), dev), float(max_norm),
                    None if outs is None else _at(outs), _raw_stream(stream, dev),
-                   keep=(ptrs, sizes, dts, outs))
+                   keep=(ptrs, sizes, dts, outs, grads, out))
