@@ -253,8 +253,10 @@ class MoELayer:
         w_gate, w_up [G][dff][d] and w_down [G][d][dff], dense, of grad_dtype (the
         weights' type, or fp32).  dx holds what came through the experts, plus
         addend [T][d] if given (the router's part, d_logits times its weights, or
-        a residual's).  grads: a dict of w_gate, w_up and w_down to add the
-        weights' gradients to, as over several micro-batches.
+        a residual's).  grads: a dict of w_gate, w_up and w_down, each of the
+        weights' type or fp32, to add the weights' gradients to, as over several
+        micro-batches (grad_dtype is not asked then); with weights=False nothing
+        is added.
 
         bf16 or fp32 layers (not fp8, whose weights are quantised).  Only d_out, x
         as permuted, Y and h are kept from the forward pass: the gate and up
@@ -270,6 +272,9 @@ class MoELayer:
                              % (self.act_dtype, T, d))
         dt, dev, f32 = self.act_dtype, self.device, torch.float32
         rows = self.x_perm.shape[0]
+        shapes = {"w_down": (G, d, dff), "w_gate": (G, dff, d), "w_up": (G, dff, d)}
+        if weights and grads is not None:
+            self._check_sums(grads, shapes)  # (before the first is added to)
 
         def new(*shape, dtype=dt):
             return torch.empty(shape, dtype=dtype, device=dev)
@@ -292,13 +297,29 @@ class MoELayer:
         api.moe_permute_backward(dx_perm, self.flat_to_row, out["dx"], self.k, n_shared=ns,
                                  addend=addend)
         if weights:
-            for name, dC, A, shape in (("w_down", dY, self.h, (G, d, dff)),
-                                       ("w_gate", gate, self.x_perm, (G, dff, d)),
-                                       ("w_up", up, self.x_perm, (G, dff, d))):
-                out[name] = new(*shape, dtype=grad_dtype or dt) if grads is None else grads[name]
+            for name, dC, A in (("w_down", dY, self.h), ("w_gate", gate, self.x_perm),
+                                ("w_up", up, self.x_perm)):
+                out[name] = (new(*shapes[name], dtype=grad_dtype or dt) if grads is None
+                             else grads[name])
                 api.moe_grouped_gemm_wgrad(dC, A, out[name], self.offsets,
                                            accumulate=grads is not None)
         return out
+
+    def _check_sums(self, grads, shapes):
+        """Refuses a dict of sums that backward() could not add all of its
+        gradients to: a call that adds some and then fails cannot be repeated."""
+        for name, shape in shapes.items():
+            t = grads.get(name)
+            if t is None:
+                raise ValueError("grads must hold %s" % name)
+            if t.dtype not in (self.act_dtype, torch.float32):
+                raise TypeError("grads[%r] must be %s or %s, got %s"
+                                % (name, self.act_dtype, torch.float32, t.dtype))
+            if t.shape != shape or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("grads[%r] must be a contiguous %s on %s, got %s on %s"
+                                 % (name, list(shape), self.device, list(t.shape), t.device))
+        if grads["w_gate"].data_ptr() == grads["w_up"].data_ptr():
+            raise ValueError("grads must hold w_gate and w_up in tensors of their own")
 
     @staticmethod
     def _agreed(balance, name, given):
