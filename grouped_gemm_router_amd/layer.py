@@ -78,6 +78,7 @@ class MoELayer:
             self.w_down = padded_weights(w_down)
         self._T = None
         self._gen = 0  # bumped whenever alloc() replaces the buffers
+        self._run_gen = 0  # of the buffers that a forward pass was last made for
         self._fwd_key, self._fwd_steps = None, None
 
     def _quant(self, w):
@@ -153,6 +154,7 @@ class MoELayer:
         next alloc() with another T replaces them)."""
         ns = self.n_shared
         d = api.deferred
+        self._run_gen = self._gen
         s = [("route", d(api.moe_route, x, self.w_router, self.topk_idx, self.topk_w,
                          logits=self.logits, logit_bias=self.bias, flags=self.flags,
                          prob_sums=self.prob_sums, ws=self.ws)),
@@ -258,10 +260,12 @@ class MoELayer:
         micro-batches (grad_dtype is not asked then); with weights=False nothing
         is added.
 
-        bf16 or fp32 layers (not fp8, whose weights are quantised).  Only d_out, x
-        as permuted, Y and h are kept from the forward pass: the gate and up
-        products are computed again.  A forward of other tokens in between
-        replaces them."""
+        bf16 or fp32 layers (not fp8, whose weights are quantised).  Only the
+        routing, x as permuted, Y and h are kept from the forward pass: the gate
+        and up products are computed again.  They are the layer's own buffers: any
+        forward in between replaces what they hold (of as many tokens without a
+        sign of it here), and one of another number of tokens replaces the
+        buffers, also for a captured call, whose replays need them as they were."""
         if self.fp8:
             raise RuntimeError("backward needs bf16 or fp32 expert weights")
         if self._T is None:
@@ -270,6 +274,8 @@ class MoELayer:
         if d_out.shape != (T, d) or d_out.dtype != self.act_dtype:
             raise ValueError("d_out must be %s [%d][%d], like the last forward's output"
                              % (self.act_dtype, T, d))
+        if self._run_gen != self._gen:
+            raise RuntimeError("backward needs a forward pass of these %d tokens before it" % T)
         dt, dev, f32 = self.act_dtype, self.device, torch.float32
         rows = self.x_perm.shape[0]
         shapes = {"w_down": (G, d, dff), "w_gate": (G, dff, d), "w_up": (G, dff, d)}

@@ -73,3 +73,20 @@ def test_sums_that_fit_are_passed_on(calls, monkeypatch, dt):
     assert len(added) == 3 and all(acc for _, acc in added)
     assert {id(t) for t, _ in added} == {id(grads[n]) for n in SHAPES}
     assert all(out[n] is grads[n] for n in SHAPES)
+
+
+def test_buffers_that_no_forward_has_written_are_refused(calls, monkeypatch):
+    """alloc() alone, and alloc() for other tokens after a forward pass."""
+    m = layer()
+    with pytest.raises(RuntimeError, match="forward pass"):
+        m.backward(torch.zeros((T, D), dtype=BF))
+    forward(m, monkeypatch)
+    m.backward(torch.zeros((T, D), dtype=BF))
+    made = len(calls)
+    m.alloc(T + 1)
+    with pytest.raises(RuntimeError, match="forward pass"):
+        m.backward(torch.zeros((T + 1, D), dtype=BF))
+    assert len(calls) == made
+    forward(m, monkeypatch)
+    m.backward(torch.zeros((T + 1, D), dtype=BF))
+    assert len(calls) == 2 * made
