@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <memory>
 #include <new>
 
@@ -529,6 +530,30 @@ hipError_t launch_wgrad(const GradArgs &a, hipStream_t s) {
   return e == hipSuccess && a.slices > 1 ? launch_wgrad_reduce(a, s) : e;
 }
 
+// An array of a call; one that is not given, or has no bytes, meets nothing.
+struct Array {
+  const void *p;
+  size_t bytes;
+};
+
+// Whether `out` overlaps one of the others.
+bool meets(const Array &out, std::initializer_list<Array> others) {
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out.p);
+  for (const Array &a : others) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p);
+    if (out.p && a.p && out.bytes && a.bytes && o < p + a.bytes && p < o + out.bytes) return true;
+  }
+  return false;
+}
+
+// `a`, or nothing where `out` is the same array, which it may be.
+Array unless_same(const Array &a, const Array &out) { return {a.p == out.p ? nullptr : a.p, a.bytes}; }
+
+// [G][N] weight rows of K elements, ldb apart
+Array weight_array(const void *B, int G, int N, int K, int ldb, moe_dtype_t dt) {
+  return {B, (((size_t)G * N - 1) * ldb + K) * size_of(dt)};
+}
+
 // bytes of n slices of `outputs` fp32 sums (none for one slice)
 size_t slice_bytes(int n, size_t outputs) { return n > 1 ? n * outputs * sizeof(float) : 0; }
 
@@ -602,7 +627,13 @@ moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void 
   if (!aligned16(d_out) || !aligned4(flat_to_row) || !aligned4(topk_w) || !opt_aligned16(dY) ||
       !opt_aligned4(d_topk_w) || (d_topk_w ? !aligned16(Y) : Y != nullptr))
     return MOE_ERR_INVALID;
-  if (dY && (dY == d_out || dY == Y)) return MOE_ERR_INVALID;
+  const size_t rows = (size_t)T * (k + n_shared), gates = (size_t)T * k * sizeof(float);
+  const Array grad = {d_out, (size_t)T * d * size_of(dt)}, y = {Y, rows * d * size_of(y_dt)};
+  const Array index = {flat_to_row, rows * sizeof(int32_t)}, w = {topk_w, gates};
+  const Array to_y = {dY, rows * d * size_of(dt)}, to_w = {d_topk_w, gates};
+  if (meets(to_y, {grad, y, index, w, to_w}) ||
+      meets(to_w, {grad, y, index, unless_same(w, to_w)}))
+    return MOE_ERR_INVALID;
   return launched(launch_combine_backward(d_out, dt, Y, y_dt, flat_to_row, topk_w, T, k, d,
                                           n_shared, dY, d_topk_w, as_stream(stream)));
 }
@@ -617,7 +648,11 @@ moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
   if (T == 0) return MOE_OK;
   if (!aligned16(dx_perm) || !aligned4(flat_to_row) || !opt_aligned16(addend) || !aligned16(dx))
     return MOE_ERR_INVALID;
-  if (dx == dx_perm) return MOE_ERR_INVALID;
+  const size_t rows = (size_t)T * (k + n_shared), bytes = (size_t)T * d * size_of(dt);
+  const Array to = {dx, bytes};
+  if (meets(to, {{dx_perm, rows * d * size_of(p_dt)}, {flat_to_row, rows * sizeof(int32_t)},
+                 unless_same({addend, bytes}, to)}))
+    return MOE_ERR_INVALID;
   return launched(launch_permute_backward(dx_perm, p_dt, flat_to_row, T, k, d, n_shared, addend, dx,
                                           dt, as_stream(stream)));
 }
@@ -640,10 +675,15 @@ moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *d
   if (!aligned16(dC) || !aligned16(B) || !opt_aligned16(dC2) || !opt_aligned16(B2) ||
       !aligned16(dA) || !aligned4(offsets))
     return MOE_ERR_INVALID;
-  if (dA == dC || dA == dC2) return MOE_ERR_INVALID;
-  const moe_status_t space = grad_workspace(
-      ws, ws_bytes, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt));
+  const size_t need = moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt);
+  const moe_status_t space = grad_workspace(ws, ws_bytes, need);
   if (space != MOE_OK) return space;
+  const size_t c_bytes = (size_t)rows * N * size_of(dt);
+  const Array c = {dC, c_bytes}, c2 = {dC2, c_bytes}, index = {offsets, (G + 1) * sizeof(int32_t)};
+  const Array b = weight_array(B, G, N, K, ldb, dt), b2 = weight_array(B2, G, N, K, ldb, dt);
+  const Array to = {dA, (size_t)rows * K * size_of(a_dt)}, work = {ws, need};
+  if (meets(to, {c, c2, b, b2, index, work}) || meets(work, {c, c2, b, b2, index}))
+    return MOE_ERR_INVALID;
   GradArgs a;
   a.dC = dC, a.dC2 = dC2, a.B = B, a.B2 = B2, a.out = dA, a.offsets = offsets;
   a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb, a.dt = dt, a.out_dt = a_dt;
@@ -662,12 +702,17 @@ moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dt
   if (!aligned16(dC) || !aligned16(B) || !aligned16(gate) || !aligned16(up) || !aligned16(d_gate) ||
       !aligned16(d_up) || !opt_aligned16(h) || !aligned4(offsets))
     return MOE_ERR_INVALID;
-  if (d_gate == dC || d_up == dC || d_gate == d_up || d_gate == up || d_up == gate)
-    return MOE_ERR_INVALID;
-  if (h && (h == dC || h == gate || h == up || h == d_gate || h == d_up)) return MOE_ERR_INVALID;
-  const moe_status_t space = grad_workspace(
-      ws, ws_bytes, moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt));
+  const size_t need = moe_grouped_gemm_dgrad_workspace_size(G, rows, N, K, dt);
+  const moe_status_t space = grad_workspace(ws, ws_bytes, need);
   if (space != MOE_OK) return space;
+  const size_t bytes = (size_t)rows * K * size_of(dt);
+  const Array c = {dC, (size_t)rows * N * size_of(dt)}, index = {offsets, (G + 1) * sizeof(int32_t)};
+  const Array b = weight_array(B, G, N, K, ldb, dt), z = {gate, bytes}, u = {up, bytes};
+  const Array to_z = {d_gate, bytes}, to_u = {d_up, bytes}, to_h = {h, bytes}, work = {ws, need};
+  if (meets(to_z, {c, b, index, unless_same(z, to_z), u, to_u, to_h, work}) ||
+      meets(to_u, {c, b, index, z, unless_same(u, to_u), to_h, work}) ||
+      meets(to_h, {c, b, index, z, u, work}) || meets(work, {c, b, index, z, u}))
+    return MOE_ERR_INVALID;
   GradArgs a;
   a.dC = dC, a.B = B, a.gate = gate, a.up = up, a.out = d_gate, a.out2 = d_up, a.h = h;
   a.offsets = offsets, a.G = G, a.rows = rows, a.N = N, a.K = K, a.ldb = ldb;
@@ -692,10 +737,13 @@ moe_status_t moe_grouped_gemm_wgrad(const void *dC, const void *A, moe_dtype_t d
   if (b_dt != dt && b_dt != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (rows > 0 && (!aligned16(dC) || !aligned16(A))) return MOE_ERR_INVALID;
   if (!aligned16(dB) || !aligned4(offsets)) return MOE_ERR_INVALID;
-  if (dB == dC || dB == A) return MOE_ERR_INVALID;
-  const moe_status_t space = grad_workspace(
-      ws, ws_bytes, moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, dt));
+  const size_t need = moe_grouped_gemm_wgrad_workspace_size(G, rows, N, K, dt);
+  const moe_status_t space = grad_workspace(ws, ws_bytes, need);
   if (space != MOE_OK) return space;
+  const Array c = {dC, (size_t)rows * N * size_of(dt)}, a_rows = {A, (size_t)rows * K * size_of(dt)};
+  const Array index = {offsets, (G + 1) * sizeof(int32_t)}, work = {ws, need};
+  const Array to = {dB, (size_t)G * N * K * size_of(b_dt)};
+  if (meets(to, {c, a_rows, index, work}) || meets(work, {c, a_rows, index})) return MOE_ERR_INVALID;
   if (rows == 0 && accumulate) return MOE_OK;
   GradArgs a;
   a.dC = dC, a.A = A, a.out = dB, a.offsets = offsets;
@@ -716,6 +764,9 @@ moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const
   if (!aligned4(norm)) return MOE_ERR_INVALID;
   if (ws_bytes < grad_norm_ws_bytes(n)) return MOE_ERR_WORKSPACE;
   if (n > 0 && (!ws || reinterpret_cast<uintptr_t>(ws) % 8 != 0)) return MOE_ERR_INVALID;
+  for (int i = 0; i < n; ++i)
+    if (meets({ws, grad_norm_ws_bytes(n)}, {{grads[i], (size_t)sizes[i] * size_of(dts[i])}}))
+      return MOE_ERR_INVALID;
   static_assert(sizeof(moe_dtype_t) == sizeof(int), "types are passed on as ints");
   return launched(launch_grad_norm(grads, sizes, reinterpret_cast<const int *>(dts), n, norm, ws,
                                    as_stream(stream)));

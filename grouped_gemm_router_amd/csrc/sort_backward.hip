@@ -76,8 +76,8 @@ __device__ __forceinline__ void token_rows(const int32_t *flat_to_row, int t, in
 template <int GS, int YS>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const void *__restrict__ d_out, const void *__restrict__ Y,
-    const int32_t *__restrict__ flat_to_row, const float *__restrict__ topk_w, int T, int k, int d,
-    int n_shared, void *__restrict__ dY, float *__restrict__ d_topk_w) {
+    const int32_t *__restrict__ flat_to_row, const float *topk_w, int T, int k, int d, int n_shared,
+    void *__restrict__ dY, float *d_topk_w) {  // (the last may be topk_w: a token's are read first)
   __shared__ int s_row[kMaxTerms];
   __shared__ float s_w[kMaxTerms];
   __shared__ float s_dot[kMaxThreads / kWave][kDots];

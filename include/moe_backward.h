@@ -19,7 +19,10 @@
  * aligned unless stated, sizes checked on the host before anything is
  * launched, work only enqueued on `stream`, nothing allocated, bit-identical
  * results for the same inputs on the same device.  Sums are held in fp32 or
- * more and rounded once, when they are stored.
+ * more and rounded once, when they are stored.  An output may be an operand
+ * only where its entry says so; one that overlaps an operand, another output
+ * or the workspace otherwise, be it in part, is MOE_ERR_INVALID (arrays are
+ * counted with all their rows, those of no group too).
  */
 #ifndef MOE_BACKWARD_H
 #define MOE_BACKWARD_H
@@ -44,7 +47,7 @@ extern "C" {
  * d_out [T][d] and dY [T k + n_shared T][d] of type dt (MOE_F32 or MOE_BF16),
  * Y of type y_dt (either) as moe_combine read it; topk_w, d_topk_w [T][k]
  * fp32.  dY may be NULL, or d_topk_w with Y (a frozen router): that part is
- * then not computed; not both.  dY may not be d_out or Y.
+ * then not computed; not both.  d_topk_w may be topk_w.
  * Requires d % 8 == 0, 1 <= k <= MOE_MAX_TOPK, n_shared <= 8.
  */
 moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void *Y,
@@ -80,7 +83,7 @@ moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
  *
  * dC, dC2 [rows][N] and B, B2 [G][N][ldb] of type dt (ldb: row pitch of the
  * weights as in moe_grouped_gemm, 0 means K), dA [rows][K] of type a_dt: dt
- * or MOE_F32.  dA may not be dC or dC2.  ws (device, 16-byte aligned) must
+ * or MOE_F32.  ws (device, 16-byte aligned) must
  * hold moe_grouped_gemm_dgrad_workspace_size bytes (else MOE_ERR_WORKSPACE;
  * NULL with ws_bytes 0 where that is 0); calls that share it must be ordered.
  * Few tiles with long sums are cut along N; the slices' fp32 sums lie in ws and
@@ -103,7 +106,7 @@ moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *d
  *   d_up[r][k]   = a * gate * s
  *   h[r][k]      = gate * s * up          (only if h is given)
  * gate, up, d_gate, d_up and h [rows][K] are of type dt.  d_gate may be gate,
- * and d_up may be up; h may be neither of those four, and none may be dC.
+ * and d_up may be up.
  * Everything else as moe_grouped_gemm_dgrad.
  */
 moe_status_t moe_grouped_gemm_dgrad_swiglu(const void *dC, const void *B, moe_dtype_t dt,
