@@ -487,8 +487,8 @@ bool opt_aligned16(const void *p) { return !p || aligned16(p); }
 moe_status_t sort_sizes(int T, int k, int d, int n_shared) {
   if (T < 0 || k < 1 || d < 8 || n_shared < 0) return MOE_ERR_INVALID;
   if (k > MOE_MAX_TOPK || n_shared > 8 || d % 8 != 0) return MOE_ERR_UNSUPPORTED;
-  // (rows are 32-bit, and a launch has fewer than 2^32 threads)
-  if ((long long)T * (k + n_shared) > INT32_MAX || T >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // (a launch has fewer than 2^32 threads; at most 40 rows a token are 32-bit)
+  if (T >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

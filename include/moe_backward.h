@@ -48,7 +48,7 @@ extern "C" {
  * Y of type y_dt (either) as moe_combine read it; topk_w, d_topk_w [T][k]
  * fp32.  dY may be NULL, or d_topk_w with Y (a frozen router): that part is
  * then not computed; not both.  d_topk_w may be topk_w.
- * Requires d % 8 == 0, 1 <= k <= MOE_MAX_TOPK, n_shared <= 8.
+ * Requires d % 8 == 0, 1 <= k <= MOE_MAX_TOPK, n_shared <= 8, T < 2^24.
  */
 moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void *Y,
                                   moe_dtype_t y_dt, const int32_t *flat_to_row,
@@ -64,7 +64,7 @@ moe_status_t moe_combine_backward(const void *d_out, moe_dtype_t dt, const void 
  * dx_perm [T k + n_shared T][d] of type p_dt, dx [T][d] of type dt and
  * addend [T][d] of type dt or NULL (what reached x by another path: the
  * router's part, or a residual's); addend may be dx.
- * Requires d % 8 == 0, 1 <= k <= MOE_MAX_TOPK, n_shared <= 8.
+ * Requires d % 8 == 0, 1 <= k <= MOE_MAX_TOPK, n_shared <= 8, T < 2^24.
  */
 moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
                                   const int32_t *flat_to_row, int T, int k, int d, int n_shared,
@@ -89,8 +89,9 @@ moe_status_t moe_permute_backward(const void *dx_perm, moe_dtype_t p_dt,
  * Few tiles with long sums are cut along N; the slices' fp32 sums lie in ws and
  * are added in a fixed order.
  * Requires N % 8 == 0, K % 8 == 0, N and ldb < MOE_MAX_GRAD_WIDTH,
- * 1 <= G <= MOE_MAX_GROUPS, and fewer than 2^24 tiles of 64 x 64 outputs
- * ((rows / 64 + G) K / 64; for the weights G N K / 4096).
+ * 1 <= G <= MOE_MAX_GROUPS, G N ldb < 2^40, and fewer than 2^24 tiles of 64 x
+ * 64 outputs ((rows / 64 + G) K / 64, and for the weights, of both calls, G N
+ * K / 4096, each side in whole tiles).
  */
 #define MOE_MAX_GRAD_WIDTH (1 << 23)
 moe_status_t moe_grouped_gemm_dgrad(const void *dC, const void *B, const void *dC2,
