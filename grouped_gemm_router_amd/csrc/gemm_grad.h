@@ -166,9 +166,10 @@ struct Span {
 // wave waits for another: 16-byte piece p of row r lies at p ^ (r & 15), which
 // spreads both the writes (32 rows of one piece) and the reads (whole rows)
 // over all banks.
-// What begin() loads is asked for DEPTH batches ahead: a load behind a store is
-// not back before the store is, and stores take microseconds (with the loads of
-// each batch behind the stores of the one before, a tile's epilogue took 10 us).
+// What begin() loads is asked for DEPTH batches ahead, behind the stores of the
+// batch then done: a load behind a store is not back before the store is, and
+// stores take microseconds (asked for one batch ahead, behind the stores that it
+// then waited for, a tile's epilogue took 10 us).
 template <bool FULL, int ROWS, int MI, int NB, class Out>
 __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *mine, const Out &out) {
   constexpr int W = NB * 32, PPR = W / 4;      // columns and 16-byte pieces a row
@@ -188,9 +189,8 @@ __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *m
       held[b % DEPTH][n] = out.template begin<FULL>(row0 + id / (W / C), col0 + id % (W / C) * C);
     }
   };
-  // (all but two batches once the first blocks have left their registers)
 #pragma unroll
-  for (int b = 0; b < (2 < BATCHES ? 2 : BATCHES); ++b) begin(b);
+  for (int b = 0; b < (DEPTH < BATCHES ? DEPTH : BATCHES); ++b) begin(b);
 #pragma unroll
   for (int b = 0; b < BATCHES; ++b) {
     if (b % (ALL / UN) == 0) {
@@ -206,11 +206,6 @@ __device__ __forceinline__ void each_piece(const f32x16 (&acc)[MI][NB], u32x4 *m
             const f32x4 v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
             mine[row * PPR + (p ^ (row & 15))] = __builtin_bit_cast(u32x4, v);
           }
-    }
-    if (b == 0) {
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int n = 2; n < (DEPTH < BATCHES ? DEPTH : BATCHES); ++n) begin(n);
     }
     float v[UN][C];
 #pragma unroll
