@@ -15,13 +15,14 @@
 //     testing every load (that arithmetic, 10 instructions a load, no longer
 //     fitted beside the MFMAs); the second of two products follows in the same
 //     run of stages.
-// Measured on that shape: 750-820 us, from card to card, 1.17-1.28 PFLOP/s (the library's
+// Measured on that shape: 750-880 us, from card to card, 1.09-1.28 PFLOP/s (the library's
 // dense product of the same sizes 1.31, its 8192^3 with both operands along the
-// sum 1.51).  The matrix cores are busy 69 % of the cycles, at 1.69 GHz: the
+// sum 1.51).  The matrix cores are busy 66 % of the cycles, at 1.70 GHz: the
 // chip lowers its clock under this load, so that fewer stalls buy less than
-// their share.  SwiGLU's gradient adds 230 us there: 1.17 GB read and written
-// (230 us at 5.05 TB/s) by waves that do nothing else meanwhile.  Measured and
-// not kept for it: eight waves of 128 x 64 (no faster, the product 3 % slower),
+// their share.  SwiGLU's gradient reads and writes 0.94 GB more than the product
+// does (186 us at 5.05 TB/s) and adds 137 us to it, 100 without h, in turn in one
+// process (813, 950 and 914 us); a workgroup does nothing else meanwhile.
+// Measured and not kept for it: eight waves of 128 x 64 (no faster, the product 3 % slower),
 // two workgroups a CU of 256 x 128 tiles (1136 against 989 us at the time),
 // loads asked for further ahead (no change, then spills), workgroups started
 // apart (1078 -> 1068 at best), 32 instead of 16 columns of tiles in turn.
