@@ -764,9 +764,12 @@ moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const
   if (!aligned4(norm)) return MOE_ERR_INVALID;
   if (ws_bytes < grad_norm_ws_bytes(n)) return MOE_ERR_WORKSPACE;
   if (n > 0 && (!ws || reinterpret_cast<uintptr_t>(ws) % 8 != 0)) return MOE_ERR_INVALID;
-  for (int i = 0; i < n; ++i)
-    if (meets({ws, grad_norm_ws_bytes(n)}, {{grads[i], (size_t)sizes[i] * size_of(dts[i])}}))
-      return MOE_ERR_INVALID;
+  const Array work = {ws, grad_norm_ws_bytes(n)}, to = {norm, sizeof(float)};
+  if (meets(to, {work})) return MOE_ERR_INVALID;
+  for (int i = 0; i < n; ++i) {
+    const Array g = {grads[i], (size_t)sizes[i] * size_of(dts[i])};
+    if (meets(g, {work, to})) return MOE_ERR_INVALID;
+  }
   static_assert(sizeof(moe_dtype_t) == sizeof(int), "types are passed on as ints");
   return launched(launch_grad_norm(grads, sizes, reinterpret_cast<const int *>(dts), n, norm, ws,
                                    as_stream(stream)));

@@ -138,3 +138,9 @@ def test_norm(lib):
         for ws in (at, at + (size - 1) // 8 * 8, at - need + 8):
             assert lib.moe_grad_norm(ptrs, n, dts, 3, C.c_void_p(BASE - FAR), C.c_void_p(ws), need,
                                      NUL) == INVALID
+        for norm in (at, at + (size - 1) // 4 * 4):  # (the norm itself, on a gradient)
+            assert lib.moe_grad_norm(ptrs, n, dts, 3, C.c_void_p(norm), C.c_void_p(BASE - FAR), need,
+                                     NUL) == INVALID
+    for norm in (BASE - FAR, BASE - FAR + need - 4):  # on the workspace
+        assert lib.moe_grad_norm(ptrs, n, dts, 3, C.c_void_p(norm), C.c_void_p(BASE - FAR), need,
+                                 NUL) == INVALID
