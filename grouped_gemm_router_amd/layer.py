@@ -324,8 +324,8 @@ class MoELayer:
             if t.shape != shape or not t.is_contiguous() or t.device != self.device:
                 raise ValueError("grads[%r] must be a contiguous %s on %s, got %s on %s"
                                  % (name, list(shape), self.device, list(t.shape), t.device))
-        if grads["w_gate"].data_ptr() == grads["w_up"].data_ptr():
-            raise ValueError("grads must hold w_gate and w_up in tensors of their own")
+        if len({grads[name].data_ptr() for name in shapes}) < len(shapes):
+            raise ValueError("grads must hold w_gate, w_up and w_down in tensors of their own")
 
     @staticmethod
     def _agreed(balance, name, given):

@@ -60,6 +60,9 @@ def test_sums_that_do_not_fit_are_refused_before_anything_is_added(calls, monkey
     one = torch.zeros(SHAPES["w_gate"])
     with pytest.raises(ValueError, match="their own"):
         m.backward(d_out, grads=sums(w_gate=one, w_up=one))
+    down = torch.zeros(SHAPES["w_down"])
+    with pytest.raises(ValueError, match="their own"):
+        m.backward(d_out, grads=sums(w_down=down, w_up=down.view(SHAPES["w_up"])))
     assert calls == []
 
 
